@@ -84,7 +84,8 @@ typedef enum {
     RAT_ERR_UNSUPPORTED = 2, /* valid request with no kernel in this library (e.g. d not 64/128) */
     RAT_ERR_CUDA = 3,        /* a CUDA runtime call or a kernel launch failed */
     RAT_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (rat_check_status) */
-    RAT_ERR_WORKSPACE = 5    /* ws_bytes below rat_workspace_size() */
+    RAT_ERR_WORKSPACE = 5,   /* ws_bytes below rat_workspace_size() */
+    RAT_ERR_NO_PAGES = 6     /* a page table needs more pages than its free list holds (rat_check_status) */
 } rat_status;
 
 typedef enum { RAT_F32 = 0, RAT_BF16 = 1 } rat_dtype;
@@ -96,7 +97,9 @@ typedef enum {
     RAT_OP_MIX = 2,           /* rat_mix_prefill with kt = vt = NULL (K~/V~ kept in ws) */
     RAT_OP_MIX_CALLER_KV = 3, /* rat_mix_prefill with caller-provided kt and vt */
     RAT_OP_DECODE = 4,        /* rat_decode_step */
-    RAT_OP_TOPK_DECODE = 5    /* rat_topk_decode_step */
+    RAT_OP_TOPK_DECODE = 5,   /* rat_topk_decode_step */
+    RAT_OP_TREE = 6,          /* rat_tree_decode_step (cfg->T nodes per entry) */
+    RAT_OP_STATUS = 7         /* calls that only record errors: rat_tree_commit, rat_page_table_update, rat_slot_map */
 } rat_op;
 
 /*
@@ -351,6 +354,127 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
                                         float *state_v, void *cache_k, void *cache_v, int cache_cap,
                                         float *stats, const int32_t *pos, void *o, float *lse, int32_t *sel,
                                         void *ws, size_t ws_bytes, rat_stream_t stream);
+
+/*
+ * Decoding with drafted tokens (speculative decoding).  A drafter proposes a
+ * tree of candidate continuations of every sequence; one step scores all of its
+ * nodes, the caller picks the branch to keep, and a commit appends it.  The
+ * step of a tree that is one chain gives what as many decode steps would give,
+ * and a tree step followed by a commit leaves cache and state as they do.
+ *
+ * Trees.  cfg->T is N, the nodes of an entry (1 <= N <= 64); token tensors are
+ * [B, N, H, d].  parent is DEVICE int32 [B, N]: parent[b, i] in [0, i) is the
+ * node above node i, -1 makes it a child of the last held position (several
+ * nodes may be), and RAT_NODE_ABSENT marks padding: such a node has no
+ * children, its inputs may hold anything (NaN too), and its outputs are o = 0,
+ * lse = -inf.  With n_i ancestors, node i is at position pos[b] + n_i, which
+ * must be below cache_cap.  An entry whose parents or positions are out of
+ * range is skipped (the step: o = 0, lse = -inf for all its nodes; the commit:
+ * state and position as they were) and RAT_ERR_INVALID recorded for
+ * rat_check_status.  cfg->t0 and t_cap are ignored.
+ */
+#define RAT_NODE_ABSENT (-2)
+#define RAT_TREE_MAX_NODES 64
+
+/*
+ * Attention of every node of the trees (as rat_decode_step for each, its
+ * sequence being the held positions and the node's branch):
+ *   s_i = a_i*s_p + (1-a_i)*x_i for x = k and v, p the parent (the entry's state
+ *   for -1); the node's augmented key/value is s_i rounded to cfg->dtype;
+ *   o[b,i,h] = merged attention of q over the held rows and the branch's nodes
+ *   of the node's dilated set and window (dilation, window, flags as there).
+ *   q, k, v, g   in  [B,N,H,d]  (g [2,B,N,H,d] with separate gates)
+ *   state_k/v    in  [B,H,d] fp32, after position pos[b]-1; not changed
+ *   cache_k/v    in  as rat_decode_step, rows of positions < pos[b]; not changed
+ *   pos          in  DEVICE int32 [B], 0 <= pos[b] <= cache_cap
+ *   o            out [B,N,H,d];  lse out [B,H,N] fp32 or NULL
+ * ws: rat_workspace_size(cfg, RAT_OP_TREE, cache_cap) bytes.  Two kernels, no
+ * other CUDA call after the first on a device: a step can be captured in a
+ * CUDA graph and replayed with parents, positions and inputs refreshed in
+ * place.  Results do not depend on the order in which the GPU runs the work.
+ */
+RAT_API rat_status rat_tree_decode_step(const rat_cfg *cfg, const void *q, const void *k, const void *v,
+                                        const void *g, const int32_t *parent, const float *state_k,
+                                        const float *state_v, const void *cache_k, const void *cache_v,
+                                        int cache_cap, const int32_t *pos, void *o, float *lse, void *ws,
+                                        size_t ws_bytes, rat_stream_t stream);
+
+/* rat_tree_decode_step over a paged cache.  A (b, h) whose step touches an
+ * invalid page is skipped (o = 0, lse = -inf) and RAT_ERR_INVALID recorded. */
+RAT_API rat_status rat_tree_decode_step_paged(const rat_cfg *cfg, const void *q, const void *k, const void *v,
+                                              const void *g, const int32_t *parent, const float *state_k,
+                                              const float *state_v, const rat_paged_cache *cache, int cache_cap,
+                                              const int32_t *pos, void *o, float *lse, void *ws, size_t ws_bytes,
+                                              rat_stream_t stream);
+
+/*
+ * Append the branch that ends at node leaf[b] (DEVICE int32 [B], -1: none) to
+ * entry b: its m nodes take positions pos[b] .. pos[b]+m-1, their augmented
+ * rows are written to the cache, out_state is the state after the leaf and
+ * out_pos[b] = pos[b] + m.  parent, k, v, g, state and pos are those of the
+ * tree step; out_state_k/v and out_pos may be the same memory as state_k/v and
+ * pos (not otherwise overlapping).  Rows of other positions are left alone.
+ * ws: rat_workspace_size(cfg, RAT_OP_STATUS, 0) bytes.  One kernel.
+ */
+RAT_API rat_status rat_tree_commit(const rat_cfg *cfg, const void *k, const void *v, const void *g,
+                                   const int32_t *parent, const int32_t *leaf, const float *state_k,
+                                   const float *state_v, float *out_state_k, float *out_state_v, void *cache_k,
+                                   void *cache_v, int cache_cap, const int32_t *pos, int32_t *out_pos, void *ws,
+                                   size_t ws_bytes, rat_stream_t stream);
+
+/* rat_tree_commit to a paged cache.  An entry whose branch touches an invalid
+ * page is skipped as a whole and RAT_ERR_INVALID recorded. */
+RAT_API rat_status rat_tree_commit_paged(const rat_cfg *cfg, const void *k, const void *v, const void *g,
+                                         const int32_t *parent, const int32_t *leaf, const float *state_k,
+                                         const float *state_v, float *out_state_k, float *out_state_v,
+                                         const rat_paged_cache *cache, int cache_cap, const int32_t *pos,
+                                         int32_t *out_pos, void *ws, size_t ws_bytes, rat_stream_t stream);
+
+/*
+ * Bring a page table in line with the sequences' lengths, on the GPU.  Entry b
+ * is to hold n = min(length[b] + extra, cache_cap) positions, none when
+ * length[b] < 0 (a finished sequence; it may be served to a new one later).  A
+ * page of its logical rows is needed when some head keeps one of positions
+ * 0 .. n-1 there (rat_cache_rows layout).  A page that the table names and that
+ * is not needed goes back to the free stack, a needed one that it does not name
+ * is taken from it, the others stay; unneeded entries become -1.  Pages are
+ * given back first, then taken, both in the order of the table's entries.
+ *   cfg          B, H, dil, win, flags; T and the token sizes are not used
+ *   page_table   in/out DEVICE int32 [B, pages_per_seq]; an entry outside
+ *                [0, num_pages) names no page
+ *   length       in  DEVICE int32 [B], <= cache_cap (else the entry is left as
+ *                it is and RAT_ERR_INVALID recorded);  extra >= 0
+ *   free_pages   in/out DEVICE int32 [num_pages], a stack of which the first
+ *                n_free[0] are free pages, the next to be taken last
+ *   n_free       in/out DEVICE int32 [1]
+ * When the stack runs out the remaining needed entries become -1 (the calls
+ * that would read them report them) and RAT_ERR_NO_PAGES is recorded; a stack
+ * that would overflow changes nothing and records RAT_ERR_INVALID.
+ * ws: rat_workspace_size(cfg, RAT_OP_STATUS, 0) bytes.  One kernel, no host
+ * synchronisation.  B * pages_per_seq < 2^31.
+ */
+RAT_API rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int page_rows, int pages_per_seq,
+                                         int num_pages, int cache_cap, const int32_t *length, int extra,
+                                         int32_t *free_pages, int32_t *n_free, void *ws, size_t ws_bytes,
+                                         rat_stream_t stream);
+
+/*
+ * Slot map: where the rows of positions pos[b] .. pos[b]+count[b]-1 are, for
+ * callers' own kernels and indexing (copying a prefix, moving rows between
+ * pools).  cfg->T is the width of the map, count[b] <= T (NULL: T everywhere).
+ *   slots        out DEVICE int64 [B,T,H]: row of the cache viewed as rows of d
+ *                elements ([B*H*R, d], or the pool as [num_pages*H*page_rows, d])
+ *                that holds the position of head h; -1 where there is none (past
+ *                count[b], off the fixed grid, a page the table does not name)
+ *   ring_slots   out DEVICE int64 [B,T,H] or NULL: under the fixed grid, its
+ *                row in the window ring, for the last W_h positions of the run; else -1
+ *   cache        NULL for the dense cache; of a paged one, table and sizes are used
+ * An entry with pos or count out of range ([0, cache_cap]) gets -1 throughout
+ * and RAT_ERR_INVALID is recorded.  ws as rat_page_table_update.
+ */
+RAT_API rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int cache_cap, const int32_t *pos,
+                                const int32_t *count, int64_t *slots, int64_t *ring_slots, void *ws,
+                                size_t ws_bytes, rat_stream_t stream);
 
 /*
  * Synchronises `stream`, returns the first device-side error recorded in `ws`

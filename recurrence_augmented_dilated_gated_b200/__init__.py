@@ -18,19 +18,23 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "librat.so")
 
-RAT_OK, RAT_ERR_INVALID, RAT_ERR_UNSUPPORTED, RAT_ERR_CUDA, RAT_ERR_TIMEOUT, RAT_ERR_WORKSPACE = range(6)
+RAT_OK, RAT_ERR_INVALID, RAT_ERR_UNSUPPORTED, RAT_ERR_CUDA, RAT_ERR_TIMEOUT, RAT_ERR_WORKSPACE, RAT_ERR_NO_PAGES = range(7)
 RAT_F32, RAT_BF16 = 0, 1
 RAT_OP_SCAN, RAT_OP_ATTN, RAT_OP_MIX, RAT_OP_MIX_CALLER_KV, RAT_OP_DECODE, RAT_OP_TOPK_DECODE = range(6)
+RAT_OP_TREE, RAT_OP_STATUS = 6, 7
 RAT_TOPK_QUEST, RAT_TOPK_MOBA = 0, 1
 RAT_FLAG_GRID_DILATION = 1
 RAT_FLAG_DEDUPE = 2
 RAT_FLAG_SEPARATE_GATES = 4
+RAT_NODE_ABSENT = -2
+RAT_TREE_MAX_NODES = 64
 
 EXPORTS = ["rat_workspace_size", "rat_workspace_init", "rat_cache_rows", "rat_scan_prefill",
            "rat_dilated_attn_prefill", "rat_mix_prefill", "rat_decode_step", "rat_check_status",
            "rat_status_string", "rat_last_error", "rat_version", "rat_launch_count", "rat_debug_set_scan_stall",
            "rat_decode_step_noalloc", "rat_topk_stats_size", "rat_topk_build_stats", "rat_topk_decode_step",
-           "rat_scan_prefill_paged", "rat_decode_step_paged"]
+           "rat_scan_prefill_paged", "rat_decode_step_paged", "rat_tree_decode_step", "rat_tree_decode_step_paged",
+           "rat_tree_commit", "rat_tree_commit_paged", "rat_page_table_update", "rat_slot_map"]
 
 
 class RatError(RuntimeError):
@@ -40,7 +44,7 @@ class RatError(RuntimeError):
 
 
 STATUS_NAMES = {0: "RAT_OK", 1: "RAT_ERR_INVALID", 2: "RAT_ERR_UNSUPPORTED", 3: "RAT_ERR_CUDA",
-                4: "RAT_ERR_TIMEOUT", 5: "RAT_ERR_WORKSPACE"}
+                4: "RAT_ERR_TIMEOUT", 5: "RAT_ERR_WORKSPACE", 6: "RAT_ERR_NO_PAGES"}
 
 
 class rat_cfg(ctypes.Structure):
@@ -85,6 +89,12 @@ def load_library(path=LIB_PATH):
     pcp = ctypes.POINTER(rat_paged_cache)
     lib.rat_scan_prefill_paged.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, pcp, I, P, S, P]
     lib.rat_decode_step_paged.argtypes = [cfgp, P, P, P, P, P, P, pcp, I, P, P, P, P, S, P]
+    lib.rat_tree_decode_step.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, I, P, P, P, P, S, P]
+    lib.rat_tree_decode_step_paged.argtypes = [cfgp, P, P, P, P, P, P, P, pcp, I, P, P, P, P, S, P]
+    lib.rat_tree_commit.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, P, P, I, P, P, P, S, P]
+    lib.rat_tree_commit_paged.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, pcp, I, P, P, P, S, P]
+    lib.rat_page_table_update.argtypes = [cfgp, P, I, I, I, I, P, I, P, P, P, S, P]
+    lib.rat_slot_map.argtypes = [cfgp, pcp, I, P, P, P, P, P, S, P]
     lib.rat_check_status.argtypes = [P, P]
     lib.rat_status_string.argtypes = [I]
     lib.rat_status_string.restype = ctypes.c_char_p
@@ -96,7 +106,8 @@ def load_library(path=LIB_PATH):
     for name in ("rat_workspace_init", "rat_scan_prefill", "rat_dilated_attn_prefill", "rat_mix_prefill",
                  "rat_decode_step", "rat_check_status", "rat_debug_set_scan_stall", "rat_decode_step_noalloc",
                  "rat_topk_build_stats", "rat_topk_decode_step", "rat_scan_prefill_paged",
-                 "rat_decode_step_paged"):
+                 "rat_decode_step_paged", "rat_tree_decode_step", "rat_tree_decode_step_paged", "rat_tree_commit",
+                 "rat_tree_commit_paged", "rat_page_table_update", "rat_slot_map"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -335,8 +346,10 @@ def paged_cache(cfg, pool_k, pool_v, page_table, cache_cap):
     _ptr(page_table, "page_table", torch.int32)
     if page_table.dim() != 2 or page_table.shape[0] != c.B:
         raise ValueError("page_table must be [B, pages_per_seq]")
-    return rat_paged_cache(pool_k.data_ptr(), pool_v.data_ptr(), page_table.data_ptr(), int(P),
+    desc = rat_paged_cache(pool_k.data_ptr(), pool_v.data_ptr(), page_table.data_ptr(), int(P),
                            int(page_table.shape[1]), int(n))
+    desc.device, desc.tensors = pool_k.device, (pool_k, pool_v, page_table)   # they live as long as the descriptor
+    return desc
 
 
 def rat_scan_prefill_paged(cfg, k, v, g, init_k=None, init_v=None, kt=None, vt=None, final_k=None, final_v=None,
@@ -366,6 +379,134 @@ def rat_decode_step_paged(cfg, q, k, v, g, state_k, state_v, cache, cache_cap, p
             _ptr(lse, "lse", torch.float32, (c.B, c.H), True), _ptr(ws, "ws", torch.uint8), ws.numel(),
             _stream(stream)]
     _check(load_library().rat_decode_step_paged(cfg.ref(), *args), "rat_decode_step_paged")
+
+
+# ------------------------------------------------------------- drafted trees
+
+
+class _Args:
+    """Arguments of one call: checked tensors of one device, on which it runs."""
+
+    def __init__(self, ws):
+        if not isinstance(ws, torch.Tensor) or ws.device.type != "cuda":
+            raise ValueError("ws must be a CUDA tensor (the library has no CPU path)")
+        self.device = ws.device
+        self.ws = _ptr(ws, "ws", torch.uint8)
+        self.ws_bytes = ws.numel()
+
+    def ptr(self, t, name, dtype, shape, optional=False):
+        if t is not None and isinstance(t, torch.Tensor) and t.device != self.device and t.numel() > 0:
+            raise ValueError("%s is on %s, the workspace on %s" % (name, t.device, self.device))
+        return _ptr(t, name, dtype, shape, optional)
+
+    def call(self, fn, what, *args, stream=None):
+        if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
+        with torch.cuda.device(self.device):
+            _check(fn(*args, self.ws, self.ws_bytes, _stream(stream)), what)
+
+
+def _paged_desc(a, cfg, cache):
+    """The descriptor of a paged cache, its tensors on the call's device."""
+    if not isinstance(cache, rat_paged_cache):
+        raise TypeError("cache must be a rat_paged_cache (paged_cache())")
+    if getattr(cache, "device", a.device) != a.device:
+        raise ValueError("cache is on %s, the workspace on %s" % (cache.device, a.device))
+    return ctypes.byref(cache)
+
+
+def _tree_step(what, cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse, ws, stream):
+    c = cfg.c
+    tok, st, dt = (c.B, c.T, c.H, c.d), (c.B, c.H, c.d), cfg.torch_dtype
+    a = _Args(ws)
+    if isinstance(cache, tuple):
+        cshape = (c.B, c.H, rat_cache_rows(cfg, cache_cap), c.d)
+        where = [a.ptr(cache[0], "cache_k", dt, cshape), a.ptr(cache[1], "cache_v", dt, cshape)]
+    else:
+        where = [_paged_desc(a, cfg, cache)]
+    a.call(getattr(load_library(), what), what, cfg.ref(), a.ptr(q, "q", dt, tok), a.ptr(k, "k", dt, tok),
+           a.ptr(v, "v", dt, tok), a.ptr(g, "g", dt, cfg.gate_shape(tok)),
+           a.ptr(parent, "parent", torch.int32, (c.B, c.T)), a.ptr(state_k, "state_k", torch.float32, st),
+           a.ptr(state_v, "state_v", torch.float32, st), *where, int(cache_cap),
+           a.ptr(pos, "pos", torch.int32, (c.B,)), a.ptr(o, "o", dt, tok),
+           a.ptr(lse, "lse", torch.float32, (c.B, c.H, c.T), True), stream=stream)
+
+
+def rat_tree_decode_step(cfg, q, k, v, g, parent, state_k, state_v, cache_k, cache_v, cache_cap, pos, o, lse=None,
+                         ws=None, stream=None):
+    """One decode step for a tree of cfg.T drafted nodes per entry: attention of every node over the held rows and
+    its own branch.  parent: int32 [B, T] (-1: child of the last held position, RAT_NODE_ABSENT: padding).  Reads
+    state and cache, changes neither; rat_tree_commit appends the branch that was accepted."""
+    _tree_step("rat_tree_decode_step", cfg, q, k, v, g, parent, state_k, state_v, (cache_k, cache_v), cache_cap, pos,
+               o, lse, ws, stream)
+
+
+def rat_tree_decode_step_paged(cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse=None, ws=None,
+                               stream=None):
+    """rat_tree_decode_step over a paged cache (a rat_paged_cache from paged_cache())."""
+    _tree_step("rat_tree_decode_step_paged", cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse,
+               ws, stream)
+
+
+def _tree_commit(what, cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache, cache_cap, pos,
+                 out_pos, ws, stream):
+    c = cfg.c
+    tok, st, dt = (c.B, c.T, c.H, c.d), (c.B, c.H, c.d), cfg.torch_dtype
+    f32, i32 = torch.float32, torch.int32
+    a = _Args(ws)
+    if isinstance(cache, tuple):
+        cshape = (c.B, c.H, rat_cache_rows(cfg, cache_cap), c.d)
+        where = [a.ptr(cache[0], "cache_k", dt, cshape), a.ptr(cache[1], "cache_v", dt, cshape)]
+    else:
+        where = [_paged_desc(a, cfg, cache)]
+    a.call(getattr(load_library(), what), what, cfg.ref(), a.ptr(k, "k", dt, tok), a.ptr(v, "v", dt, tok),
+           a.ptr(g, "g", dt, cfg.gate_shape(tok)), a.ptr(parent, "parent", i32, (c.B, c.T)),
+           a.ptr(leaf, "leaf", i32, (c.B,)), a.ptr(state_k, "state_k", f32, st), a.ptr(state_v, "state_v", f32, st),
+           a.ptr(out_state_k, "out_state_k", f32, st), a.ptr(out_state_v, "out_state_v", f32, st), *where,
+           int(cache_cap), a.ptr(pos, "pos", i32, (c.B,)), a.ptr(out_pos, "out_pos", i32, (c.B,)), stream=stream)
+
+
+def rat_tree_commit(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache_k, cache_v,
+                    cache_cap, pos, out_pos, ws=None, stream=None):
+    """Append the branch ending at node leaf[b] (int32 [B], -1: none): its rows to the cache, the state after it to
+    out_state, the new length to out_pos (state and pos may be updated in place)."""
+    _tree_commit("rat_tree_commit", cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v,
+                 (cache_k, cache_v), cache_cap, pos, out_pos, ws, stream)
+
+
+def rat_tree_commit_paged(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache, cache_cap,
+                          pos, out_pos, ws=None, stream=None):
+    """rat_tree_commit to a paged cache (a rat_paged_cache from paged_cache())."""
+    _tree_commit("rat_tree_commit_paged", cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v,
+                 cache, cache_cap, pos, out_pos, ws, stream)
+
+
+def rat_page_table_update(cfg, page_table, page_rows, num_pages, cache_cap, length, extra, free_pages, n_free, ws=None,
+                          stream=None):
+    """Bring page_table (int32 [B, pages_per_seq]) in line with entries of length[b] + extra positions (length < 0:
+    none), taking pages from and giving them back to the stack free_pages[:n_free[0]].  In place, on the GPU."""
+    c = cfg.c
+    a = _Args(ws)
+    i32 = torch.int32
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != c.B:
+        raise ValueError("page_table must be [B, pages_per_seq]")
+    a.call(load_library().rat_page_table_update, "rat_page_table_update", cfg.ref(),
+           a.ptr(page_table, "page_table", i32, None), int(page_rows), int(page_table.shape[1]), int(num_pages),
+           int(cache_cap), a.ptr(length, "length", i32, (c.B,)), int(extra),
+           a.ptr(free_pages, "free_pages", i32, (int(num_pages),)), a.ptr(n_free, "n_free", i32, (1,)), stream=stream)
+
+
+def rat_slot_map(cfg, cache, cache_cap, pos, count, slots, ring_slots=None, ws=None, stream=None):
+    """Rows (int64 [B, T, H]) of positions pos[b] .. pos[b]+count[b]-1 in the cache seen as rows of d elements; cache
+    is None for the dense one, or a rat_paged_cache.  count None: cfg.T positions everywhere."""
+    c = cfg.c
+    a = _Args(ws)
+    shape = (c.B, c.T, c.H)
+    a.call(load_library().rat_slot_map, "rat_slot_map", cfg.ref(),
+           None if cache is None else _paged_desc(a, cfg, cache), int(cache_cap),
+           a.ptr(pos, "pos", torch.int32, (c.B,)), a.ptr(count, "count", torch.int32, (c.B,), True),
+           a.ptr(slots, "slots", torch.int64, shape), a.ptr(ring_slots, "ring_slots", torch.int64, shape, True),
+           stream=stream)
 
 
 def rat_check_status(ws, stream=None):

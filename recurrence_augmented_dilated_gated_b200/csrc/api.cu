@@ -10,7 +10,9 @@
 #include <atomic>
 
 #include "attn_tc.cuh"
+#include "pages.cuh"
 #include "rat_internal.cuh"
+#include "tree.cuh"
 
 using namespace rat;
 
@@ -110,11 +112,34 @@ int64_t cache_rows(const rat_cfg *c, int cap) {
     return R;
 }
 
+// cfg of a call that decodes: t0 and t_cap say nothing there and are dropped.
+rat_status check_step_cfg(const rat_cfg *c, rat_cfg *out) {
+    if (!c) return fail(RAT_ERR_INVALID, "cfg is NULL");
+    *out = *c;
+    out->t0 = out->t_cap = 0;
+    return check_cfg(out);
+}
+
+// Sizes of a tree step or commit.  The plan's counts are bounded here, so that
+// grids and row numbers fit in 32 bits.
+rat_status check_tree(const rat_cfg *c, int cap) {
+    if (c->T < 1) return fail(RAT_ERR_INVALID, "a tree needs at least one node (T = %d)", c->T);
+    if (c->T > kTreeMaxNodes) return fail(RAT_ERR_UNSUPPORTED, "T = %d exceeds %d nodes", c->T, kTreeMaxNodes);
+    if (cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cap);
+    TreeParams p;
+    tree_plan(c, cap, &p);
+    const long long most = std::max((long long)p.ctas_per_b, (long long)c->H * c->T);
+    if ((double)c->B * (double)most >= 2147483647.0)
+        return fail(RAT_ERR_UNSUPPORTED, "B = %d entries are too many for one tree step", c->B);
+    return RAT_OK;
+}
+
 struct Layout {
     size_t ticket = 0, flags = 0, agg = 0, incl = 0;  // scan
     size_t lse_dil = 0, att_ticket = 0;               // attention
     size_t kt = 0, vt = 0;                            // mix scratch
     size_t part = 0;                                  // decode
+    size_t tree = 0;                                  // tree step
     int nchunks = 0, items_per_b = 0;
     size_t total = 0;
 };
@@ -147,6 +172,11 @@ Layout layout(const rat_cfg *c, int op, int cap) {
         L.part = off;
         off = align256(off + decode_plan(c, cap, &tmp));
         L.items_per_b = tmp.items_per_b;
+    }
+    if (op == RAT_OP_TREE) {
+        TreeParams tmp;
+        L.tree = off;
+        off = align256(off + tree_plan(c, cap, &tmp).total);
     }
     L.total = off;
     return L;
@@ -601,13 +631,21 @@ const char *rat_status_string(rat_status s) {
     case RAT_ERR_CUDA: return "RAT_ERR_CUDA: CUDA runtime or launch failure";
     case RAT_ERR_TIMEOUT: return "RAT_ERR_TIMEOUT: a bounded device-side wait gave up";
     case RAT_ERR_WORKSPACE: return "RAT_ERR_WORKSPACE: workspace too small";
+    case RAT_ERR_NO_PAGES: return "RAT_ERR_NO_PAGES: the free list ran out of pages";
     }
     return "unknown rat_status";
 }
 
 size_t rat_workspace_size(const rat_cfg *cfg, int op, int cache_cap) {
-    if (op < RAT_OP_SCAN || op > RAT_OP_TOPK_DECODE) return 0;
+    if (op < RAT_OP_SCAN || op > RAT_OP_STATUS) return 0;
     const bool dec = op == RAT_OP_DECODE || op == RAT_OP_TOPK_DECODE;
+    if (op == RAT_OP_TREE || op == RAT_OP_STATUS) {
+        rat_cfg tmp;
+        if (check_step_cfg(cfg, &tmp) != RAT_OK) return 0;
+        if (op == RAT_OP_STATUS) return sizeof(WsHeader);
+        if (check_tree(&tmp, cache_cap) != RAT_OK) return 0;
+        return layout(&tmp, op, cache_cap).total;
+    }
     if (check_cfg(cfg, !dec) != RAT_OK) return 0;
     if (dec && cache_cap < 1) return 0;
     if (op == RAT_OP_TOPK_DECODE) return sizeof(WsHeader);   // the status word only
@@ -793,6 +831,225 @@ rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk, int mod
     p.hdr = reinterpret_cast<WsHeader *>(ws);
     cudaError_t e = launch_topk_decode(p, cfg->dtype, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "top-k decode launch");
+    return RAT_OK;
+}
+
+// ------------------------------------------------------------ drafted trees
+
+namespace {
+
+void set_paged(const rat_paged_cache *pc, const int *&table, int &page_rows, int &pps, int &num_pages) {
+    table = pc ? pc->page_table : nullptr;
+    page_rows = pc ? pc->page_rows : 0;
+    pps = pc ? pc->pages_per_seq : 0;
+    num_pages = pc ? pc->num_pages : 0;
+}
+
+// rat_tree_decode_step with a dense cache (pc = NULL) or a paged one.
+rat_status tree_step(const rat_cfg *cfg_in, const void *q, const void *k, const void *v, const void *g,
+                     const int32_t *parent, const float *state_k, const float *state_v, const void *cache_k,
+                     const void *cache_v, const rat_paged_cache *pc, int cache_cap, const int32_t *pos, void *o,
+                     float *lse, void *ws, size_t ws_bytes, rat_stream_t stream) {
+    rat_cfg c;
+    rat_status st = check_step_cfg(cfg_in, &c);
+    if (st != RAT_OK) return st;
+    st = check_tree(&c, cache_cap);
+    if (st != RAT_OK) return st;
+    if (c.B == 0) return RAT_OK;
+    CHECK_PTR(q, "q"); CHECK_PTR(k, "k"); CHECK_PTR(v, "v"); CHECK_PTR(g, "g"); CHECK_PTR(parent, "parent");
+    CHECK_PTR(state_k, "state_k"); CHECK_PTR(state_v, "state_v");
+    CHECK_PTR(cache_k, "cache_k"); CHECK_PTR(cache_v, "cache_v");
+    CHECK_PTR(pos, "pos"); CHECK_PTR(o, "o"); CHECK_OPT(lse, "lse");
+    Layout L;
+    st = check_ws(&c, RAT_OP_TREE, cache_cap, ws, ws_bytes, &L);
+    if (st != RAT_OK) return st;
+    TreeParams p;
+    memset(&p, 0, sizeof(p));
+    const TreeLayout tl = tree_plan(&c, cache_cap, &p);
+    p.q = q; p.k = k; p.v = v; p.g = g;
+    p.parent = parent;
+    p.state[0] = state_k; p.state[1] = state_v;
+    p.cache[0] = cache_k; p.cache[1] = cache_v;
+    set_paged(pc, p.page_table, p.page_rows, p.pps, p.num_pages);
+    p.pos = pos; p.o = o; p.lse = lse;
+    char *w = static_cast<char *>(ws) + L.tree;
+    p.node_rows = w + tl.node_rows;
+    p.part = reinterpret_cast<float *>(w + tl.part);
+    p.ml = reinterpret_cast<float2 *>(w + tl.ml);
+    p.cap = cache_cap; p.B = c.B; p.N = c.T; p.H = c.H; p.d = c.d;
+    p.scale_log2 = scale_of(&c) * 1.4426950408889634f;
+    p.hdr = reinterpret_cast<WsHeader *>(ws);
+    cudaError_t e = launch_tree(p, c.dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "tree step launch");
+    return RAT_OK;
+}
+
+// rat_tree_commit with a dense cache (pc = NULL) or a paged one.
+rat_status tree_commit(const rat_cfg *cfg_in, const void *k, const void *v, const void *g, const int32_t *parent,
+                       const int32_t *leaf, const float *state_k, const float *state_v, float *out_state_k,
+                       float *out_state_v, void *cache_k, void *cache_v, const rat_paged_cache *pc, int cache_cap,
+                       const int32_t *pos, int32_t *out_pos, void *ws, size_t ws_bytes, rat_stream_t stream) {
+    rat_cfg c;
+    rat_status st = check_step_cfg(cfg_in, &c);
+    if (st != RAT_OK) return st;
+    st = check_tree(&c, cache_cap);
+    if (st != RAT_OK) return st;
+    if (c.B == 0) return RAT_OK;
+    CHECK_PTR(k, "k"); CHECK_PTR(v, "v"); CHECK_PTR(g, "g"); CHECK_PTR(parent, "parent"); CHECK_PTR(leaf, "leaf");
+    CHECK_PTR(state_k, "state_k"); CHECK_PTR(state_v, "state_v");
+    CHECK_PTR(out_state_k, "out_state_k"); CHECK_PTR(out_state_v, "out_state_v");
+    CHECK_PTR(cache_k, "cache_k"); CHECK_PTR(cache_v, "cache_v");
+    CHECK_PTR(pos, "pos"); CHECK_PTR(out_pos, "out_pos");
+    Layout L;
+    st = check_ws(&c, RAT_OP_STATUS, 0, ws, ws_bytes, &L);
+    if (st != RAT_OK) return st;
+    CommitParams p;
+    memset(&p, 0, sizeof(p));
+    p.k = k; p.v = v; p.g = g;
+    p.parent = parent; p.leaf = leaf;
+    p.state[0] = state_k; p.state[1] = state_v;
+    p.out_state[0] = out_state_k; p.out_state[1] = out_state_v;
+    p.cache[0] = cache_k; p.cache[1] = cache_v;
+    p.pos = pos; p.out_pos = out_pos;
+    p.cache_R = cache_rows(&c, cache_cap);
+    p.cap = cache_cap; p.B = c.B; p.N = c.T; p.H = c.H; p.d = c.d;
+    p.grid = grid_mode(&c) ? 1 : 0;
+    p.sep = separate_gates(&c) ? 1 : 0;
+    set_paged(pc, p.page_table, p.page_rows, p.pps, p.num_pages);
+    for (int h = 0; h < c.H; ++h) {
+        p.dil[h] = c.dil[h];
+        p.win[h] = c.win[h];
+        p.slab[h] = (int)(((long long)cache_cap + c.dil[h] - 1) / c.dil[h]);
+        p.recur[h] = head_recur(&c, h) ? 1 : 0;
+    }
+    p.hdr = reinterpret_cast<WsHeader *>(ws);
+    cudaError_t e = launch_tree_commit(p, c.dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "tree commit launch");
+    return RAT_OK;
+}
+
+rat_status check_paged_step(const rat_cfg *cfg, const rat_paged_cache *pc, int cap) {
+    rat_cfg c;
+    rat_status st = check_step_cfg(cfg, &c);
+    return st != RAT_OK ? st : check_paged(&c, pc, cap);
+}
+
+}  // namespace
+
+rat_status rat_tree_decode_step(const rat_cfg *cfg, const void *q, const void *k, const void *v, const void *g,
+                                const int32_t *parent, const float *state_k, const float *state_v,
+                                const void *cache_k, const void *cache_v, int cache_cap, const int32_t *pos, void *o,
+                                float *lse, void *ws, size_t ws_bytes, rat_stream_t stream) {
+    return tree_step(cfg, q, k, v, g, parent, state_k, state_v, cache_k, cache_v, nullptr, cache_cap, pos, o, lse, ws,
+                     ws_bytes, stream);
+}
+
+rat_status rat_tree_decode_step_paged(const rat_cfg *cfg, const void *q, const void *k, const void *v, const void *g,
+                                      const int32_t *parent, const float *state_k, const float *state_v,
+                                      const rat_paged_cache *cache, int cache_cap, const int32_t *pos, void *o,
+                                      float *lse, void *ws, size_t ws_bytes, rat_stream_t stream) {
+    rat_status st = check_paged_step(cfg, cache, cache_cap);
+    if (st != RAT_OK) return st;
+    return tree_step(cfg, q, k, v, g, parent, state_k, state_v, cache->pool_k, cache->pool_v, cache, cache_cap, pos, o,
+                     lse, ws, ws_bytes, stream);
+}
+
+rat_status rat_tree_commit(const rat_cfg *cfg, const void *k, const void *v, const void *g, const int32_t *parent,
+                           const int32_t *leaf, const float *state_k, const float *state_v, float *out_state_k,
+                           float *out_state_v, void *cache_k, void *cache_v, int cache_cap, const int32_t *pos,
+                           int32_t *out_pos, void *ws, size_t ws_bytes, rat_stream_t stream) {
+    return tree_commit(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache_k, cache_v,
+                       nullptr, cache_cap, pos, out_pos, ws, ws_bytes, stream);
+}
+
+rat_status rat_tree_commit_paged(const rat_cfg *cfg, const void *k, const void *v, const void *g,
+                                 const int32_t *parent, const int32_t *leaf, const float *state_k,
+                                 const float *state_v, float *out_state_k, float *out_state_v,
+                                 const rat_paged_cache *cache, int cache_cap, const int32_t *pos, int32_t *out_pos,
+                                 void *ws, size_t ws_bytes, rat_stream_t stream) {
+    rat_status st = check_paged_step(cfg, cache, cache_cap);
+    if (st != RAT_OK) return st;
+    return tree_commit(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache->pool_k,
+                       cache->pool_v, cache, cache_cap, pos, out_pos, ws, ws_bytes, stream);
+}
+
+rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int page_rows, int pages_per_seq,
+                                 int num_pages, int cache_cap, const int32_t *length, int extra,
+                                 int32_t *free_pages, int32_t *n_free, void *ws, size_t ws_bytes,
+                                 rat_stream_t stream) {
+    rat_cfg c;
+    rat_status st = check_step_cfg(cfg, &c);
+    if (st != RAT_OK) return st;
+    if (page_rows < 1 || num_pages < 1 || pages_per_seq < 1)
+        return fail(RAT_ERR_INVALID, "page_rows %d, num_pages %d, pages_per_seq %d must be >= 1", page_rows, num_pages,
+                    pages_per_seq);
+    if (cache_cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cache_cap);
+    if (extra < 0) return fail(RAT_ERR_INVALID, "extra %d < 0", extra);
+    const long long R = cache_rows(&c, cache_cap);
+    if ((long long)pages_per_seq * page_rows < R)
+        return fail(RAT_ERR_INVALID, "pages_per_seq x page_rows < %lld cache rows", R);
+    if ((long long)c.B * pages_per_seq >= 0x7fffffffLL)
+        return fail(RAT_ERR_UNSUPPORTED, "B x pages_per_seq exceeds 2^31 entries");
+    if (c.B == 0) return RAT_OK;
+    CHECK_PTR(page_table, "page_table"); CHECK_PTR(length, "length");
+    CHECK_PTR(free_pages, "free_pages"); CHECK_PTR(n_free, "n_free");
+    Layout L;
+    st = check_ws(&c, RAT_OP_STATUS, 0, ws, ws_bytes, &L);
+    if (st != RAT_OK) return st;
+    PageUpdateParams p;
+    memset(&p, 0, sizeof(p));
+    p.table = page_table; p.length = length; p.free_pages = free_pages; p.n_free = n_free;
+    p.B = c.B; p.pps = pages_per_seq; p.page_rows = page_rows; p.num_pages = num_pages;
+    p.cap = cache_cap; p.extra = extra;
+    p.grid = grid_mode(&c) ? 1 : 0;
+    for (int h = 0; h < c.H; ++h) {
+        HeadClass k;
+        k.D = c.dil[h];
+        k.W = p.grid && k.D > 1 ? c.win[h] : 0;
+        k.S = (int)(((long long)cache_cap + k.D - 1) / k.D);
+        int i = 0;
+        while (i < p.ncls && (p.cls[i].D != k.D || p.cls[i].W != k.W)) ++i;
+        if (i == p.ncls) p.cls[p.ncls++] = k;
+    }
+    p.hdr = reinterpret_cast<WsHeader *>(ws);
+    cudaError_t e = launch_page_update(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "page table launch");
+    return RAT_OK;
+}
+
+rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int cache_cap, const int32_t *pos,
+                        const int32_t *count, int64_t *slots, int64_t *ring_slots, void *ws, size_t ws_bytes,
+                        rat_stream_t stream) {
+    rat_cfg c;
+    rat_status st = check_step_cfg(cfg, &c);
+    if (st != RAT_OK) return st;
+    if (cache) {
+        st = check_paged(&c, cache, cache_cap);
+        if (st != RAT_OK) return st;
+    }
+    if (cache_cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cache_cap);
+    if (empty(&c)) return RAT_OK;
+    CHECK_PTR(pos, "pos"); CHECK_OPT(count, "count"); CHECK_PTR(slots, "slots"); CHECK_OPT(ring_slots, "ring_slots");
+    Layout L;
+    st = check_ws(&c, RAT_OP_STATUS, 0, ws, ws_bytes, &L);
+    if (st != RAT_OK) return st;
+    SlotParams p;
+    memset(&p, 0, sizeof(p));
+    p.pos = pos; p.count = count;
+    p.slots = reinterpret_cast<long long *>(slots);
+    p.ring = reinterpret_cast<long long *>(ring_slots);
+    p.cache_R = cache_rows(&c, cache_cap);
+    p.B = c.B; p.T = c.T; p.H = c.H; p.cap = cache_cap;
+    p.grid = grid_mode(&c) ? 1 : 0;
+    set_paged(cache, p.page_table, p.page_rows, p.pps, p.num_pages);
+    for (int h = 0; h < c.H; ++h) {
+        p.dil[h] = c.dil[h];
+        p.win[h] = c.win[h];
+        p.slab[h] = (int)(((long long)cache_cap + c.dil[h] - 1) / c.dil[h]);
+    }
+    p.hdr = reinterpret_cast<WsHeader *>(ws);
+    cudaError_t e = launch_slot_map(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "slot map launch");
     return RAT_OK;
 }
 

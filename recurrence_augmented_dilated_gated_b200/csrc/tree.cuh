@@ -1,0 +1,186 @@
+// tree.cuh -- parameter block and device helpers of the drafted-tree kernels
+// (tree.cu: attention of the nodes; tree_commit.cu: the accepted branch).
+#pragma once
+
+#include "rat_internal.cuh"
+
+namespace rat {
+
+// Nodes of one entry's tree, at most: a branch fits in one 64-bit mask.
+constexpr int kTreeMaxNodes = 64;
+
+struct TreeParams {
+    const void *q, *k, *v, *g;   // [B,N,H,d]
+    const int *parent;           // device [B,N]
+    const float *state[2];       // [B,H,d] fp32, read only
+    const void *cache[2];        // [B,H,R,d] or the pools, read only
+    const int *pos;              // device [B]
+    void *o;                     // [B,N,H,d]
+    float *lse;                  // [B,H,N] or null
+    void *node_rows;             // [B][H][2][N][d] augmented rows of the nodes (cfg dtype)
+    float *part;                 // [B][slots_per_b][N][d] unnormalised accumulators
+    float2 *ml;                  // [B][slots_per_b][N] (max, sum); sum < 0: a page was not valid
+    long long cache_R;
+    int cap, B, N, H, d;
+    int grid, dedupe, sep;       // as in DecodeParams
+    const int *page_table;
+    int page_rows, pps, num_pages;
+    float scale_log2;
+    int ctas_per_b, slots_per_b;
+    int dil[kMaxHeads];
+    int win[kMaxHeads];
+    int slab[kMaxHeads];         // ceil(cap / dil)
+    int nsplit[kMaxHeads];       // pieces of one dilated set, at most
+    int wsplit[kMaxHeads];       // pieces of the window's held rows (>= 1)
+    int slab_ctas[kMaxHeads];    // CTAs that share the head's (set, piece) items
+    int cta0[kMaxHeads + 1];     // first CTA of head h within an entry
+    int slot0[kMaxHeads + 1];    // first partial slot of head h within an entry
+    unsigned char recur[kMaxHeads];
+    WsHeader *hdr;
+};
+
+// The shape of one entry's tree, in shared memory.
+struct TreeInfo {
+    unsigned long long anc[kTreeMaxNodes];  // branch of node i, itself included (0: absent)
+    int jump[kTreeMaxNodes];
+    signed char depth[kTreeMaxNodes];       // -1: absent
+    int max_depth;                          // -1: no node
+    int valid;                              // parents and position in range
+};
+
+// Depths and branches from the parents (one warp).  A node's branch is its
+// parent's and itself; pointer doubling finds it in log2(depth) rounds.
+// parent[i] is in [-1, i), or -2 for an absent node, which has no children.
+__device__ __forceinline__ void tree_analyse(TreeInfo &ti, const int *parent, int N, int pos, int cap) {
+    const int lane = threadIdx.x & 31;
+    int par[2];
+    bool ok = pos >= 0 && pos <= cap;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        par[u] = i < N ? parent[i] : -2;
+        ok = ok && par[u] >= -2 && par[u] < i;
+        ti.jump[i] = par[u];
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();
+    if (ok) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (par[u] >= 0) ok = ok && ti.jump[par[u]] != -2;
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    int dmax = -1;
+    if (ok) {
+        unsigned long long anc[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = lane + 32 * u;
+            anc[u] = par[u] == -2 ? 0ull : 1ull << i;
+            ti.anc[i] = anc[u];
+        }
+        __syncwarp();
+        while (__any_sync(0xffffffffu, par[0] >= 0 || par[1] >= 0)) {
+            int nj[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                nj[u] = par[u];
+                if (par[u] >= 0) {
+                    anc[u] |= ti.anc[par[u]];
+                    nj[u] = ti.jump[par[u]];
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = lane + 32 * u;
+                par[u] = nj[u];
+                ti.jump[i] = nj[u];
+                ti.anc[i] = anc[u];
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int dep = __popcll(anc[u]) - 1;
+            ti.depth[lane + 32 * u] = (signed char)dep;
+            dmax = max(dmax, dep);
+        }
+        dmax = __reduce_max_sync(0xffffffffu, dmax);
+        ok = pos + dmax < cap;   // every node's position has a row (pos <= cap: no overflow)
+    }
+    if (lane == 0) {
+        ti.max_depth = dmax;
+        ti.valid = ok ? 1 : 0;
+    }
+}
+
+// The dilated sets of an entry's nodes.  Positions t and t' have the same held
+// keys when t == t' mod D, so nodes are taken by depth mod D: set g holds the
+// nodes of depth == g mod D, and reads slab (pos + g) mod D.  On the fixed grid
+// (and for D = 1) every node reads the same rows.
+__device__ __forceinline__ int tree_num_sets(const TreeParams &p, int D, int max_depth) {
+    return p.grid ? (max_depth >= 0 ? 1 : 0) : min(D, max_depth + 1);
+}
+__device__ __forceinline__ int tree_set_of(const TreeParams &p, int D, int depth) {
+    return p.grid || D == 1 ? 0 : depth % D;
+}
+// Held rows of set g, and the first cache row of its slab.
+__device__ __forceinline__ int tree_set_rows(const TreeParams &p, int h, int pos, int g, long long &row0) {
+    const int D = p.dil[h];
+    if (p.grid) {
+        row0 = 0;
+        return pos / D;
+    }
+    const int r = (int)(((long long)pos + g) % D);
+    row0 = (long long)r * p.slab[h];
+    return pos > r ? (pos - 1 - r) / D + 1 : 0;
+}
+// How n rows are cut: at most `most` pieces of equal length, none shorter than
+// kTreeMinRows (but the last).
+constexpr int kTreeMinRows = 128;
+__device__ __forceinline__ int tree_piece_rows(int n, int most) {
+    const int pieces = max(1, min(most, (n + kTreeMinRows - 1) / kTreeMinRows));
+    return ((n + pieces - 1) / pieces + 15) & ~15;
+}
+
+// Gate of one channel: a = sigmoid(g) and 1 - a without cancellation, as in the
+// decode step (logits beyond +-80 saturate).
+__device__ __forceinline__ void gate_pair(float g, float &a, float &oma) {
+    const float e = expf(-fminf(fmaxf(g, -80.f), 80.f));
+    a = 1.f / (1.f + e);
+    oma = e * a;
+}
+
+// Split plan and workspace offsets of a tree step (host); returns the bytes the
+// step needs after the workspace header.
+struct TreeLayout {
+    size_t node_rows, part, ml, total;
+};
+TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p);
+
+cudaError_t launch_tree(const TreeParams &p, int dtype, cudaStream_t s);
+
+// Commit of the accepted branch (tree_commit.cu).
+struct CommitParams {
+    const void *k, *v, *g;       // [B,N,H,d]
+    const int *parent, *leaf;    // device [B,N], [B]
+    const float *state[2];       // [B,H,d] fp32
+    float *out_state[2];         // [B,H,d] fp32, may be the same memory
+    void *cache[2];              // [B,H,R,d] or the pools
+    const int *pos;              // device [B]
+    int *out_pos;                // device [B], may be the same memory
+    long long cache_R;
+    int cap, B, N, H, d;
+    int grid, sep;
+    const int *page_table;
+    int page_rows, pps, num_pages;
+    int dil[kMaxHeads];
+    int win[kMaxHeads];
+    int slab[kMaxHeads];
+    unsigned char recur[kMaxHeads];
+    WsHeader *hdr;
+};
+cudaError_t launch_tree_commit(const CommitParams &p, int dtype, cudaStream_t s);
+
+}  // namespace rat

@@ -21,7 +21,7 @@
 //     64-bit mask); a long window is cut into further items.
 // tree_combine_kernel joins the partials in a fixed order.
 // Bound: the cache rows, each read once; 4 d operations per (node, row).
-#include "tree.cuh"
+#include "tree_keys.cuh"
 
 namespace rat {
 
@@ -29,58 +29,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 32;   // keys per shared-memory tile
-
-__device__ __forceinline__ int find_head(const TreeParams &p, int it) {
-    int lo = 0, hi = p.H - 1;  // largest h with cta0[h] <= it
-    while (lo < hi) {
-        int mid = (lo + hi + 1) >> 1;
-        if (p.cta0[mid] <= it) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
-// The keys of one item: rows of a slab, held rows of the window, or the nodes.
-enum KeyKind { kSlab = 0, kWindow = 1, kNodes = 2 };
-
-struct Keys {
-    int kind;
-    long long row0;   // slab: first cache row;  window: first position
-    int n;            // keys
-};
-
-__device__ __forceinline__ long long key_offset(const TreeParams &p, const Keys &ks, int b, int h, int i) {
-    if (ks.kind == kNodes) return ((((long long)b * p.H + h) * 2) * p.N + i) * p.d;   // keys; values N * d further
-    long long row = ks.row0 + i;
-    if (ks.kind == kWindow) {
-        long long main_row, ring_row;
-        cache_rows_of(row, p.dil[h], p.win[h], p.slab[h], p.grid, main_row, ring_row);
-        row = ring_row >= 0 ? ring_row : main_row;
-    }
-    return cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H, p.d, b, h, row);
-}
-
-// How often key i counts for a node of depth `dep` and branch `anc` (0, 1 or 2).
-__device__ __forceinline__ int key_count(const TreeParams &p, const Keys &ks, const TreeInfo &ti, int h, int pos,
-                                         int dep, unsigned long long anc, int node, int i) {
-    if (i >= ks.n) return 0;
-    if (ks.kind == kSlab) return 1;
-    const int D = p.dil[h], W = p.win[h];
-    if (ks.kind == kWindow) {
-        const int j = (int)ks.row0 + i, t = pos + dep;
-        if (j <= t - W) return 0;
-        if (p.dedupe && (p.grid ? j % D == D - 1 : (t - j) % D == 0)) return 0;
-        return 1;
-    }
-    if (!((anc >> i) & 1ull)) return 0;
-    const int back = dep - ti.depth[i];
-    const int far = p.grid ? (i == node || (pos + ti.depth[i]) % D == D - 1) : back % D == 0;
-    const int near = back < W && !(p.dedupe && far);
-    return far + near;
-}
-
-template <typename T> __device__ __forceinline__ T to_t(float x);
-template <> __device__ __forceinline__ float to_t<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 to_t<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // Shared memory of one CTA (floats): Q [MQ][D], K [kTile][D + 4], V [kTile][D],
 // P [MQ][kTile]; the recurrence's history [MQ][...] lies over K, V and P.
@@ -221,34 +169,6 @@ __device__ __forceinline__ void attend(const TreeParams &p, const Keys &ks, cons
     }
 }
 
-// The recurrence down the tree: one channel of one tensor per thread, nodes in
-// order (a parent comes before its children), states kept in shared memory.
-template <typename T, int D>
-__device__ __forceinline__ void run_tree(const TreeParams &p, const int *parent, int b, int h,
-                                         float *hist) {
-    const size_t bh = (size_t)b * p.H + h;
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-        const int x = i / D, c = i % D;
-        const T *src = static_cast<const T *>(x ? p.v : p.k);
-        const T *gate = static_cast<const T *>(p.g) + (p.sep && x ? (size_t)p.B * p.N * p.H * D : 0);
-        const float s0 = p.state[x][bh * D + c];
-        T *out = static_cast<T *>(p.node_rows) + (bh * 2 + x) * p.N * D + c;
-        float *hc = hist + threadIdx.x;   // this thread's column: no other thread reads it
-        const bool rec = p.recur[h] != 0;
-#pragma unroll 4
-        for (int n = 0; n < p.N; ++n) {
-            const size_t e = (((size_t)b * p.N + n) * p.H + h) * D + c;
-            float a = 0.f, oma = 1.f;
-            if (rec) gate_pair((float)gate[e], a, oma);
-            const int par = parent[n];
-            float s = a * (par >= 0 ? hc[(size_t)par * kThreads] : s0) + oma * (float)src[e];
-            if (par == RAT_NODE_ABSENT) s = 0.f;   // its inputs may hold anything
-            hc[(size_t)n * kThreads] = s;
-            out[(size_t)n * D] = to_t<T>(s);
-        }
-    }
-}
-
 template <typename T, int D, int MQ>
 __device__ __forceinline__ void run_item(const TreeParams &p, const TreeInfo &ti, int b, int h, int pos,
                                          const Keys *parts, int n_parts, int slot, const int *nodes, int n_nodes,
@@ -302,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeParams p)
     __shared__ float s_corr[kTreeMaxNodes];
     const int tid = threadIdx.x;
     const int b = blockIdx.x / p.ctas_per_b, it = blockIdx.x % p.ctas_per_b;
-    const int h = find_head(p, it), li = it - p.cta0[h];
+    const int h = find_tree_head(p, it), li = it - p.cta0[h];
     const int pos = p.pos[b];
     if (tid < 32) tree_analyse(ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
     if (tid < kTreeMaxNodes) s_parent[tid] = tid < p.N ? p.parent[(size_t)b * p.N + tid] : -2;
@@ -311,53 +231,26 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeParams p)
         if (!ti.valid && li == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
         return;
     }
-    const int D_ = p.dil[h], W = p.win[h], ws = p.wsplit[h];
+    const int ws = p.wsplit[h];
     if (li < ws) {
-        // local items: a piece of the window's held rows; item 0 also the nodes
-        const int n_held = W > 0 ? min(W - 1, pos) : 0, j0 = pos - n_held;
-        const int len = (n_held + ws - 1) / ws;
         Keys parts[2];
-        const int a = min(li * len, n_held);
-        parts[0].kind = kWindow;
-        parts[0].row0 = j0 + a;
-        parts[0].n = min(len, n_held - a);
-        parts[1].kind = kNodes;
-        parts[1].row0 = 0;
-        parts[1].n = p.N;
-        if (li == 0) {
-            // history: MQ rows of kThreads floats over Q, K, V and P
-            run_tree<T, D>(p, s_parent, b, h, smem);
-        }
+        const int n_parts = local_keys(p, h, pos, li, parts);
+        // its history: MQ rows of kThreads floats over Q, K, V and P
+        if (li == 0) run_tree<T, D, kThreads>(p, s_parent, b, h, smem);
         if (tid == 0) s_n = p.N;
         if (tid < p.N) s_nodes[tid] = tid;
         __syncthreads();
-        run_item<T, D, MQ>(p, ti, b, h, pos, parts, li == 0 ? 2 : 1, p.nsplit[h] + li, s_nodes, p.N, smem, s_corr,
+        run_item<T, D, MQ>(p, ti, b, h, pos, parts, n_parts, p.nsplit[h] + li, s_nodes, p.N, smem, s_corr,
                            s_flags);
         return;
     }
-    const int sets = tree_num_sets(p, D_, ti.max_depth), items = sets * p.nsplit[h];
+    const int sets = tree_num_sets(p, p.dil[h], ti.max_depth), items = sets * p.nsplit[h];
     for (int x = li - ws; x < items; x += p.slab_ctas[h]) {
         const int g = x % sets, piece = x / sets;
         Keys ks;
-        ks.kind = kSlab;
-        const int n = tree_set_rows(p, h, pos, g, ks.row0);
-        const int len = tree_piece_rows(n, p.nsplit[h]);
-        if (n == 0 || piece * len >= n) continue;
-        ks.row0 += piece * len;
-        ks.n = min(len, n - piece * len);
+        if (!slab_keys(p, h, pos, g, piece, ks)) continue;
         __syncthreads();
-        if (tid < 32) {
-            int cnt = 0;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int i = tid + 32 * u;
-                const bool in = ti.depth[i] >= 0 && tree_set_of(p, D_, ti.depth[i]) == g;
-                const unsigned mask = __ballot_sync(0xffffffffu, in);
-                if (in) s_nodes[cnt + __popc(mask & ((1u << tid) - 1u))] = i;
-                cnt += __popc(mask);
-            }
-            if (tid == 0) s_n = cnt;
-        }
+        if (tid < 32) list_nodes(p, ti, h, g, s_nodes, &s_n);
         __syncthreads();
         run_item<T, D, MQ>(p, ti, b, h, pos, &ks, 1, piece, s_nodes, s_n, smem, s_corr, s_flags);
     }
@@ -443,7 +336,9 @@ template <typename T, int D, int MQ> cudaError_t launch_simt(const TreeParams &p
 
 template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
     const unsigned grid = (unsigned)p.B * (unsigned)p.ctas_per_b;
-    cudaError_t e = p.N <= 16 ? launch_simt<T, D, 16>(p, grid, s) : launch_simt<T, D, 64>(p, grid, s);
+    cudaError_t e;
+    if constexpr (sizeof(T) == 2) e = launch_tree_mma(p, grid, s);
+    else e = p.N <= 16 ? launch_simt<T, D, 16>(p, grid, s) : launch_simt<T, D, 64>(p, grid, s);
     if (e != cudaSuccess) return e;
     const unsigned nb = (p.N + kCombineNodes - 1) / kCombineNodes;
     tree_combine_kernel<T, D><<<(unsigned)p.B * p.H * nb, kCombineThreads, 0, s>>>(p);

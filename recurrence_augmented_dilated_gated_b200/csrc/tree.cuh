@@ -160,6 +160,8 @@ struct TreeLayout {
 TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p);
 
 cudaError_t launch_tree(const TreeParams &p, int dtype, cudaStream_t s);
+// the attention part of a bf16 step (tree_mma.cu)
+cudaError_t launch_tree_mma(const TreeParams &p, unsigned grid, cudaStream_t s);
 
 // Commit of the accepted branch (tree_commit.cu).
 struct CommitParams {

@@ -31,7 +31,7 @@ constexpr int kThreads = 128;
 constexpr int kTile = 32;   // keys per shared-memory tile
 
 // Shared memory of one CTA (floats): Q [MQ][D], K [kTile][D + 4], V [kTile][D],
-// P [MQ][kTile]; the recurrence's history [MQ][...] lies over K, V and P.
+// P [MQ][kTile]; the recurrence's states and stage lie over them.
 template <int D, int MQ> constexpr size_t simt_floats() {
     return (size_t)MQ * D + kTile * (D + 4) + kTile * D + (size_t)MQ * kTile;
 }
@@ -235,8 +235,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeParams p)
     if (li < ws) {
         Keys parts[2];
         const int n_parts = local_keys(p, h, pos, li, parts);
-        // its history: MQ rows of kThreads floats over Q, K, V and P
-        if (li == 0) run_tree<T, D, kThreads>(p, s_parent, b, h, smem);
+        if (li == 0) run_tree<T, D>(p, s_parent, b, h, reinterpret_cast<uint8_t *>(smem));   // over Q, K, V and P
         if (tid == 0) s_n = p.N;
         if (tid < p.N) s_nodes[tid] = tid;
         __syncthreads();
@@ -325,8 +324,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
 }
 
 template <typename T, int D, int MQ> cudaError_t launch_simt(const TreeParams &p, unsigned grid, cudaStream_t s) {
-    static_assert(simt_floats<D, MQ>() >= (size_t)MQ * kThreads, "the recurrence's history fits");
-    const size_t smem = simt_floats<D, MQ>() * sizeof(float);
+    const size_t smem = simt_floats<D, MQ>() * sizeof(float) > tree_smem<D>(MQ) ? simt_floats<D, MQ>() * sizeof(float) : tree_smem<D>(MQ);
     static std::atomic<unsigned long long> smem_set{0};
     cudaError_t e = ensure_smem_limit(tree_simt_kernel<T, D, MQ>, smem, smem_set);
     if (e != cudaSuccess) return e;
@@ -367,7 +365,10 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p) {
         if (n * c->B >= kItemsWanted) break;
         target /= 2;
     }
-    int ctas = 0, slots = 0;
+    // A CTA that takes several items looks at the tree once: no more CTAs than
+    // kItemsWanted * 4 in all, however many items there are.
+    long long share = c->B > 0 ? (4ll * kItemsWanted + (long long)c->B * c->H - 1) / ((long long)c->B * c->H) : 1;
+    int ctas = 0, slots = 0, per_head = 0;
     long long R = 0;
     for (int h = 0; h < c->H; ++h) {
         const int D = c->dil[h];
@@ -380,11 +381,14 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p) {
         p->nsplit[h] = ns;
         const int w = p->win[h] < cap ? p->win[h] : cap;
         p->wsplit[h] = w > target ? (w + target - 1) / target : 1;
-        p->slab_ctas[h] = sets_of(D) * ns;
+        const long long most = (long long)sets_of(D) * ns;
+        p->slab_ctas[h] = (int)(most < share ? most : share);
         p->cta0[h] = ctas;
         p->slot0[h] = slots;
         p->recur[h] = (c->recur == nullptr || c->recur[h] != 0) ? 1 : 0;
-        ctas += p->wsplit[h] + p->slab_ctas[h];
+        const int mine = p->wsplit[h] + p->slab_ctas[h];
+        per_head = h == 0 ? mine : per_head == mine ? mine : -1;
+        ctas += mine;
         slots += ns + p->wsplit[h];
         const long long rows = grid ? (long long)slab + (D > 1 ? c->win[h] : 0) : (long long)D * slab;
         R = R > rows ? R : rows;
@@ -393,6 +397,7 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p) {
     p->slot0[c->H] = slots;
     p->ctas_per_b = ctas;
     p->slots_per_b = slots;
+    p->ctas_per_head = per_head > 0 ? per_head : 0;
     p->cache_R = R;
     p->grid = grid ? 1 : 0;
     p->dedupe = (c->flags & RAT_FLAG_DEDUPE) ? 1 : 0;

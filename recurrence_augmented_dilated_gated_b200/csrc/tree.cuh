@@ -27,6 +27,7 @@ struct TreeParams {
     int page_rows, pps, num_pages;
     float scale_log2;
     int ctas_per_b, slots_per_b;
+    int ctas_per_head;           // when all heads have as many, else 0
     int dil[kMaxHeads];
     int win[kMaxHeads];
     int slab[kMaxHeads];         // ceil(cap / dil)

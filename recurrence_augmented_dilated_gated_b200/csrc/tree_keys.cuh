@@ -8,6 +8,7 @@
 namespace rat {
 
 __device__ __forceinline__ int find_tree_head(const TreeParams &p, int it) {
+    if (p.ctas_per_head > 0) return it / p.ctas_per_head;
     int lo = 0, hi = p.H - 1;  // largest h with cta0[h] <= it
     while (lo < hi) {
         int mid = (lo + hi + 1) >> 1;
@@ -99,32 +100,79 @@ __device__ __forceinline__ void list_nodes(const TreeParams &p, const TreeInfo &
     if (lane == 0) *n = cnt;
 }
 
-// The recurrence down the tree: one channel of one tensor per thread, nodes in
-// order (a parent comes before its children), states kept in shared memory.
-template <typename T, int D, int kThreads>
-__device__ __forceinline__ void run_tree(const TreeParams &p, const int *parent, int b, int h,
-                                         float *hist) {
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes past L1; zeros when `on` is false (the address is not read then)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The recurrence down the tree (128 threads).  A thread owns one channel of both
+// tensors (D = 128) or of one (D = 64: the upper half of the CTA takes the
+// values) and walks the nodes in order, a parent before its children.  k, v and
+// g of as many nodes as fit in kTreeStage bytes are staged together by
+// asynchronous copies: one round trip to memory for 32 nodes of bf16, not one
+// per node.  Shared memory: the states, a column per thread ([node][2 D] floats),
+// then the stage.  The code is kept small (no unrolled chunk): it runs once per
+// CTA, and fetching a straight line of instructions cold costs more than the
+// loop (measured: 40 us a CTA with 16 nodes unrolled).
+constexpr int kTreeStage = 32768;
+template <int D> constexpr size_t tree_smem(int N) { return (size_t)N * 2 * D * sizeof(float) + kTreeStage; }
+
+template <typename T, int D>
+__device__ __forceinline__ void run_tree(const TreeParams &p, const int *parent, int b, int h, uint8_t *smem) {
+    constexpr int kThreads = 128, kBoth = D == kThreads ? 2 : 1;
+    constexpr int kChunks = D * (int)sizeof(T) / 16;                 // 16-byte chunks of a row
+    constexpr int kNodes = kTreeStage / (4 * D * (int)sizeof(T));    // nodes staged at a time (k, v, two gates)
+    static_assert(D * 2 == kThreads * kBoth, "the CTA's threads cover the channels of both tensors");
+    const int tid = threadIdx.x, c = tid % D, x0 = tid / D;
     const size_t bh = (size_t)b * p.H + h;
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-        const int x = i / D, c = i % D;
-        const T *src = static_cast<const T *>(x ? p.v : p.k);
-        const T *gate = static_cast<const T *>(p.g) + (p.sep && x ? (size_t)p.B * p.N * p.H * D : 0);
-        const float s0 = p.state[x][bh * D + c];
-        T *out = static_cast<T *>(p.node_rows) + (bh * 2 + x) * p.N * D + c;
-        float *hc = hist + threadIdx.x;   // this thread's column: no other thread reads it
-        const bool rec = p.recur[h] != 0;
-#pragma unroll 4
-        for (int n = 0; n < p.N; ++n) {
-            const size_t e = (((size_t)b * p.N + n) * p.H + h) * D + c;
+    const bool rec = p.recur[h] != 0;
+    const int n_src = !rec ? 2 : p.sep ? 4 : 3;
+    float *hc = reinterpret_cast<float *>(smem) + tid;   // [node][kBoth][thread]: no other thread reads this column
+    uint8_t *stage = smem + (size_t)p.N * 2 * D * sizeof(float);
+    const float s0 = p.state[x0][bh * D + c], s1 = kBoth == 2 ? p.state[1][bh * D + c] : 0.f;
+    T *out = static_cast<T *>(p.node_rows) + (bh * 2 + x0) * p.N * D + c;
+    for (int n0 = 0; n0 < p.N; n0 += kNodes) {
+        const int nn = min(kNodes, p.N - n0);
+        __syncthreads();   // the stage is free
+#pragma unroll 1
+        for (int y = 0; y < n_src; ++y) {
+            const char *src = static_cast<const char *>(y == 0 ? p.k : y == 1 ? p.v : p.g) +
+                              (y == 3 ? (size_t)p.B * p.N * p.H * D * sizeof(T) : 0);
+#pragma unroll 1
+            for (int e = tid; e < nn * kChunks; e += kThreads) {
+                const int n = e / kChunks, ch = e % kChunks;
+                cp_async16(smem_u32(stage) + ((y * kNodes + n) * kChunks + ch) * 16,
+                           src + ((((size_t)b * p.N + n0 + n) * p.H + h) * kChunks + ch) * 16, true);
+            }
+        }
+        cp_commit();
+        cp_wait<0>();
+        __syncthreads();
+        const T *st = reinterpret_cast<const T *>(stage) + c;
+#pragma unroll 2
+        for (int w = 0; w < nn; ++w) {
+            const int n = n0 + w, par = parent[n];
             float a = 0.f, oma = 1.f;
-            if (rec) gate_pair((float)gate[e], a, oma);
-            const int par = parent[n];
-            float s = a * (par >= 0 ? hc[(size_t)par * kThreads] : s0) + oma * (float)src[e];
+            if (rec) gate_pair((float)st[((p.sep && x0 ? 3 : 2) * kNodes + w) * D], a, oma);
+            float s = a * (par >= 0 ? hc[(size_t)par * kBoth * kThreads] : s0) + oma * (float)st[(x0 * kNodes + w) * D];
             if (par == RAT_NODE_ABSENT) s = 0.f;   // its inputs may hold anything
-            hc[(size_t)n * kThreads] = s;
+            hc[(size_t)n * kBoth * kThreads] = s;
             store1(out + (size_t)n * D, s);
+            if (kBoth == 2) {
+                if (rec && p.sep) gate_pair((float)st[(3 * kNodes + w) * D], a, oma);
+                s = a * (par >= 0 ? hc[(size_t)(par * 2 + 1) * kThreads] : s1) + oma * (float)st[(kNodes + w) * D];
+                if (par == RAT_NODE_ABSENT) s = 0.f;
+                hc[(size_t)(n * 2 + 1) * kThreads] = s;
+                store1(out + (size_t)(p.N + n) * D, s);
+            }
         }
     }
+    __threadfence();   // other threads copy these rows past L1
 }
 
 }  // namespace rat

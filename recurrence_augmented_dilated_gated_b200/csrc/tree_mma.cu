@@ -30,16 +30,6 @@ constexpr int kTile = 64;
 constexpr int kStages = 3;
 constexpr float kSlack = 8.f;   // log2 of how far P may pass 1
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 bytes; zeros when `on` is false (the address is not read then)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
@@ -73,13 +63,16 @@ template <int D> struct Shape {
 struct Shared {
     TreeInfo ti;
     int parent[kTreeMaxNodes], nodes[kTreeMaxNodes];
-    int n, bad;
-    unsigned long long odd[3];       // rows of local tile t with a value that is not finite, at t mod 3
+    int n, bad, odd;                      // odd: some local value is not finite
+    uint8_t count[kTreeMaxNodes][kTile];  // how often a key of a masked tile counts for a node
     float m[kWarps][16], l[kWarps][16];
 };
 
-// One item: the keys of parts[0 .. n_parts), tile by tile.
-template <int D, bool kLocal>
+// One item: the keys of parts[0 .. n_parts), tile by tile, for the sh.n nodes of
+// sh.nodes.  One body serves slabs and local items (what differs is where a row
+// is and which tiles carry a mask): a second copy of it would only thrash the
+// instruction cache.
+template <int D>
 __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_t *ring, const Keys *parts, int n_parts,
                                          int b, int h, int pos, int slot) {
     using S = Shape<D>;
@@ -89,67 +82,58 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
     const int WM = n_nodes <= 16 ? 1 : n_nodes <= 32 ? 2 : 4, WK = kWarps / WM;
     const int wm = warp % WM, wk = warp / WM;
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;   // this lane's row (and r0 + 8) and first column of a fragment
-    int tiles[2] = {(parts[0].n + kTile - 1) / kTile, n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0};
-    const int n_tiles = tiles[0] + tiles[1];
+    const int tiles0 = (parts[0].n + kTile - 1) / kTile;
+    const int n_tiles = tiles0 + (n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0);
+    if (tid == 0) sh.bad = sh.odd = 0;
 
+    // Q into the stage that no tile uses yet
+    const uint32_t sq = smem_u32(ring) + (kStages - 1) * S::kStage;
+    for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
+        const int r = e / S::kChunks, c = e % S::kChunks;
+        const bool on = r < n_nodes;
+        const int n = on ? sh.nodes[r] : 0;
+        cp_async16(sq + S::at(r, c), static_cast<const __nv_bfloat16 *>(p.q) + (((size_t)b * p.N + n) * p.H + h) * D + c * 8, on);
+    }
+    cp_commit();
     auto load = [&](int t) {
-        const Keys &ks = parts[kLocal && t >= tiles[0] ? 1 : 0];
-        const int k0 = (kLocal && t >= tiles[0] ? t - tiles[0] : t) * kTile;
-        const __nv_bfloat16 *src[2];
-        if (kLocal && ks.kind == kNodes) {
-            src[0] = static_cast<const __nv_bfloat16 *>(p.node_rows);
-            src[1] = src[0] + (size_t)p.N * D;
-        } else {
-            src[0] = static_cast<const __nv_bfloat16 *>(p.cache[0]);
-            src[1] = static_cast<const __nv_bfloat16 *>(p.cache[1]);
+        const bool second = t >= tiles0;
+        const Keys &ks = parts[second ? 1 : 0];
+        const int k0 = (second ? t - tiles0 : t) * kTile;
+        const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(p.cache[0]), *vb = static_cast<const __nv_bfloat16 *>(p.cache[1]);
+        if (ks.kind == kNodes) {
+            kb = static_cast<const __nv_bfloat16 *>(p.node_rows);
+            vb = kb + (size_t)p.N * D;
+        }
+        // a warp copies 16 rows; lane i finds the place of the i-th of them
+        constexpr int kPerPass = 32 / S::kChunks;   // rows of a warp in one pass
+        const int mine = (lane & 15) / kPerPass * S::kRowsAtOnce + warp * kPerPass + (lane & 15) % kPerPass;
+        long long off = -1;
+        if (k0 + mine < ks.n) {
+            off = key_offset(p, ks, b, h, k0 + mine);
+            if (off < 0) sh.bad = 1;
         }
         const uint32_t dst = smem_u32(ring) + (t % kStages) * S::kStage;
-        const int c = tid % S::kChunks;
+        const int c = lane % S::kChunks;
 #pragma unroll
-        for (int r = tid / S::kChunks; r < kTile; r += S::kRowsAtOnce) {
-            const bool in = k0 + r < ks.n;
-            long long off = in ? key_offset(p, ks, b, h, k0 + r) : 0;
-            const bool on = in && off >= 0;
-            if (in && off < 0) sh.bad = 1;
-            if (!on) off = 0;
-            cp_async16(dst + S::at(r, c), src[0] + off + c * 8, on);
-            cp_async16(dst + S::kHalf + S::at(r, c), src[1] + off + c * 8, on);
+        for (int i = 0; i < 16 / kPerPass; ++i) {
+            const long long o = __shfl_sync(0xffffffffu, off, i * kPerPass + lane / S::kChunks);
+            const int r = i * S::kRowsAtOnce + warp * kPerPass + lane / S::kChunks;
+            const long long e = o < 0 ? 0 : o + c * 8;
+            cp_async16(dst + S::at(r, c), kb + e, o >= 0);
+            cp_async16(dst + S::kHalf + S::at(r, c), vb + e, o >= 0);
         }
     };
-
-    if (tid == 0) sh.bad = 0;
-    if (tid < 3) sh.odd[tid] = 0;
     __syncthreads();
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < kStages - 1; ++t) {
         if (t < n_tiles) load(t);
         cp_commit();
     }
-    // the warp's nodes: rows of Q as A fragments
-    uint32_t q[D / 16][4];
-    int node[2];
+    cp_wait<kStages - 1>();
+    __syncthreads();
+    uint32_t q[D / 16][4];   // the warp's nodes: rows of Q as A fragments
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int r = wm * 16 + r0 + 8 * u;
-        node[u] = r < n_nodes ? sh.nodes[r] : -1;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(
-            static_cast<const __nv_bfloat16 *>(p.q) + (((size_t)b * p.N + max(node[u], 0)) * p.H + h) * D);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            q[k][u] = node[u] >= 0 ? src[k * 8 + (lane & 3)] : 0u;
-            q[k][u + 2] = node[u] >= 0 ? src[k * 8 + 4 + (lane & 3)] : 0u;
-        }
-    }
-    int dep[2] = {0, 0};
-    unsigned long long anc[2] = {0ull, 0ull};
-    if (kLocal) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (node[u] >= 0) {
-                dep[u] = sh.ti.depth[node[u]];
-                anc[u] = sh.ti.anc[node[u]];
-            }
-    }
+    for (int k = 0; k < D / 16; ++k) ldsm4(q[k], sq + S::at(wm * 16 + (lane & 15), 2 * k + (lane >> 4)));
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -157,36 +141,46 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // references, this lane's part of the sums
 
+#pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
         cp_wait<kStages - 2>();
-        const uint8_t *kt = ring + (t % kStages) * S::kStage;
-        const Keys &ks = parts[kLocal && t >= tiles[0] ? 1 : 0];
-        const int k0 = (kLocal && t >= tiles[0] ? t - tiles[0] : t) * kTile;
-        if (kLocal) {
-            // values that are not finite leave the tile (their keys are noted):
-            // a zero probability times one of them would reach every node
-            uint4 *v = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(kt) + S::kHalf);
-            const int c = tid % S::kChunks;
+        const uint32_t sk = smem_u32(ring) + (t % kStages) * S::kStage, sv = sk + S::kHalf;
+        const bool second = t >= tiles0;
+        const Keys &ks = parts[second ? 1 : 0];
+        const int k0 = (second ? t - tiles0 : t) * kTile;
+        // nodes mask each other; the window's first keys are out of the deeper
+        // nodes' reach; with dedupe any of its keys may be in the dilated set
+        const bool local = ks.kind != kSlab;
+        const bool masked = ks.kind == kNodes || (ks.kind == kWindow && (p.dedupe || k0 < sh.ti.max_depth));
+        if (local) {
+            // values that are not finite leave the tile: a zero probability times
+            // one of them would reach every node.  add_odd() puts them back
+            __syncwarp();
+            uint4 *v = reinterpret_cast<uint4 *>(ring + (t % kStages) * S::kStage + S::kHalf);
 #pragma unroll 1
             for (int r = tid / S::kChunks; r < kTile; r += S::kRowsAtOnce) {
-                uint4 *e = v + S::at(r, c) / 16;
-                uint4 x = *e;
+                uint4 *e = v + S::at(r, tid % S::kChunks) / 16;
+                const uint4 x = *e;
                 if (not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w)) {
-                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    for (int i = 0; i < 4; ++i) {
-                        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-                        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
-                    }
-                    *e = make_uint4(w[0], w[1], w[2], w[3]);
-                    atomicOr(&sh.odd[t % 3], 1ull << r);
+                    __nv_bfloat16 *w = reinterpret_cast<__nv_bfloat16 *>(e);
+                    for (int i = 0; i < 8; ++i)
+                        if (!(fabsf(__bfloat162float(w[i])) < INFINITY)) w[i] = __float2bfloat16_rn(0.f);
+                    sh.odd = 1;
                 }
             }
         }
         __syncthreads();   // the tile has landed for everyone, and the one before is done with
+        if (masked) {
+#pragma unroll 1
+            for (int e = tid; e < n_nodes * kTile; e += kThreads) {
+                const int i = e / kTile, key = k0 + e % kTile, dep = sh.ti.depth[i];
+                sh.count[i][e % kTile] = dep < 0 ? 0 : key_count(p, ks, sh.ti, h, pos, dep, sh.ti.anc[i], i, key);
+            }
+            __syncthreads();
+        }
         if (t + kStages - 1 < n_tiles) load(t + kStages - 1);
         cp_commit();
-        if (kLocal && tid == 0) sh.odd[(t + 2) % 3] = 0;   // read for tile t - 1, next set after tile t + 1's barrier
-        const uint32_t sk = smem_u32(kt), sv = sk + S::kHalf;
+#pragma unroll 1
         for (int kb = wk; kb < kTile / 16; kb += WK) {
             if (k0 + kb * 16 >= ks.n) break;
             float s[2][4];
@@ -203,37 +197,46 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
             }
             // s[n][2u + j]: node row r0 + 8u, key kb * 16 + 8n + c0 + j
             float cnt[2][4];
+            if (masked) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int r = wm * 16 + r0 + 8 * u;
+                        const uint16_t w = r < n_nodes ? *reinterpret_cast<const uint16_t *>(&sh.count[r][kb * 16 + 8 * n + c0]) : (uint16_t)0;
+                        cnt[n][2 * u] = (float)(w & 0xff);
+                        cnt[n][2 * u + 1] = (float)(w >> 8);
+                    }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cnt[n][j] = k0 + kb * 16 + 8 * n + c0 + (j & 1) < ks.n ? 1.f : 0.f;
+            }
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int key = k0 + kb * 16 + 8 * n + c0 + j;
-                        float w = key < ks.n ? 1.f : 0.f;
-                        if (kLocal) w = node[u] < 0 ? 0.f : (float)key_count(p, ks, sh.ti, h, pos, dep[u], anc[u], node[u], key);
-                        cnt[n][2 * u + j] = w;
-                        s[n][2 * u + j] = w > 0.f ? s[n][2 * u + j] * p.scale_log2 : -INFINITY;
-                        mx[u] = fmaxf(mx[u], s[n][2 * u + j]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    s[n][j] = cnt[n][j] > 0.f ? s[n][j] * p.scale_log2 : -INFINITY;
+                    mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
+                }
             if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
                 // some node's reference is raised (the first keys always do)
+                float corr[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
                     mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-                    if (mx[u] > m[u] + kSlack) {
-                        const float corr = exp2f(m[u] - mx[u]);   // 0 from a reference of -inf
-                        m[u] = mx[u];
-                        l[u] *= corr;
-#pragma unroll
-                        for (int i = 0; i < D / 8; ++i) {
-                            o[i][2 * u] *= corr;
-                            o[i][2 * u + 1] *= corr;
-                        }
-                    }
+                    const bool up = mx[u] > m[u] + kSlack;
+                    corr[u] = up ? exp2f(m[u] - mx[u]) : 1.f;   // 0 from a reference of -inf
+                    m[u] = up ? mx[u] : m[u];
+                    l[u] *= corr[u];
                 }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[i][j] *= corr[j >> 1];
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -241,11 +244,9 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float &x = s[n][2 * u + j];
-                        x = exp2f(x - ref);
-                        if (kLocal) x = cnt[n][2 * u + j] > 0.f ? x * cnt[n][2 * u + j] : 0.f;
-                        l[u] += x;
+                    for (int j = 2 * u; j < 2 * u + 2; ++j) {
+                        s[n][j] = cnt[n][j] > 0.f ? cnt[n][j] * exp2f(s[n][j] - ref) : 0.f;
+                        l[u] += s[n][j];
                     }
             }
             const uint32_t pa[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
@@ -258,107 +259,77 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
                 mma16816(o[2 * i], pa, f[0], f[1]);
                 mma16816(o[2 * i + 1], pa, f[2], f[3]);
             }
-            if (kLocal) {
-                unsigned odd = (unsigned)(sh.odd[t % 3] >> (kb * 16)) & 0xffffu;
-                while (odd) {
-                    // rare: the values left out above, for the nodes that see their key
-                    const int key = __ffs(odd) - 1;
-                    odd &= odd - 1;
-                    const long long off = key_offset(p, ks, b, h, k0 + kb * 16 + key);
-                    const __nv_bfloat16 *v = ks.kind == kNodes
-                                                 ? static_cast<const __nv_bfloat16 *>(p.node_rows) + (size_t)p.N * D + off
-                                                 : static_cast<const __nv_bfloat16 *>(p.cache[1]) + off;
-                    const int from = (lane & ~3) | ((key & 7) >> 1);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float lo = __shfl_sync(0xffffffffu, key < 8 ? s[0][2 * u] : s[1][2 * u], from);
-                        const float hi = __shfl_sync(0xffffffffu, key < 8 ? s[0][2 * u + 1] : s[1][2 * u + 1], from);
-                        const float pr = (key & 1) ? hi : lo;
-#pragma unroll
-                        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float x = __bfloat162float(v[i * 8 + c0 + j]);
-                                if (pr != 0.f && !(fabsf(x) < INFINITY)) o[i][2 * u + j] += pr * x;
-                            }
-                    }
-                }
-            }
         }
     }
 
-    // join the warps that hold the same nodes, then write the partial
+    // Join the warps that hold the same nodes: sums go to shared memory, scaled
+    // to the common reference, and leave it row by row.
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
         l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+        if ((lane & 3) == 0) {
+            sh.m[warp][r0 + 8 * u] = m[u];
+            sh.l[warp][r0 + 8 * u] = l[u];
+        }
     }
     cp_wait<0>();
     __syncthreads();
-    if (WK > 1) {
-        float *so = reinterpret_cast<float *>(ring);   // [warp][16][D]
-        if ((lane & 3) == 0) {
+    float *so = reinterpret_cast<float *>(ring);   // [warp][16][D], a row's columns turned by 8 r (banks)
+    float M[2], L[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                sh.m[warp][r0 + 8 * u] = m[u];
-                sh.l[warp][r0 + 8 * u] = l[u];
-            }
+    for (int u = 0; u < 2; ++u) {
+        const int r = r0 + 8 * u;
+        M[u] = -INFINITY;
+        L[u] = 0.f;
+        for (int x = 0; x < WK; ++x) M[u] = fmaxf(M[u], sh.m[x * WM + wm][r]);
+        for (int x = 0; x < WK; ++x) {
+            const float mm = sh.m[x * WM + wm][r], ll = sh.l[x * WM + wm][r];
+            L[u] += mm == -INFINITY ? ll : ll * exp2f(mm - M[u]);   // -inf: nothing seen (0), or NaN
         }
-        __syncthreads();
-        float w[2];
+        const float w = m[u] == -INFINITY ? 1.f : exp2f(m[u] - M[u]);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<float2 *>(so + (warp * 16 + r) * D + (i * 8 + c0 + 8 * r) % D) = make_float2(o[i][2 * u] * w, o[i][2 * u + 1] * w);
+    }
+    __syncthreads();
+    const size_t base = ((size_t)b * p.slots_per_b + p.slot0[h] + slot) * p.N;
+    if (wk == 0 && (lane & 3) == 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            float M = -INFINITY;
-            for (int x = 0; x < WK; ++x) M = fmaxf(M, sh.m[x * WM + wm][r0 + 8 * u]);
-            w[u] = m[u] == -INFINITY ? (l[u] == 0.f ? 0.f : 1.f) : exp2f(m[u] - M);
-            float L = 0.f;
-            for (int x = 0; x < WK; ++x) {
-                const float mm = sh.m[x * WM + wm][r0 + 8 * u], ll = sh.l[x * WM + wm][r0 + 8 * u];
-                L += mm == -INFINITY ? ll : ll * exp2f(mm - M);   // -inf: nothing seen (0), or NaN
-            }
-            m[u] = M;
-            l[u] = L;
-        }
-        if (wk > 0) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    // row-wise rotation by 8 floats a row keeps the lanes of a store on different banks
-                    const int r = r0 + 8 * u, c = (i * 8 + c0 + 8 * r) % D;
-                    *reinterpret_cast<float2 *>(so + (warp * 16 + r) * D + c) = make_float2(o[i][2 * u] * w[u], o[i][2 * u + 1] * w[u]);
-                }
-        }
-        __syncthreads();
-        if (wk == 0) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int r = r0 + 8 * u, c = (i * 8 + c0 + 8 * r) % D;
-                    float x = o[i][2 * u] * w[u], y = o[i][2 * u + 1] * w[u];
-                    for (int k = 1; k < WK; ++k) {
-                        const float2 z = *reinterpret_cast<const float2 *>(so + ((k * WM + wm) * 16 + r) * D + c);
-                        x += z.x;
-                        y += z.y;
-                    }
-                    o[i][2 * u] = x;
-                    o[i][2 * u + 1] = y;
-                }
+            const int r = wm * 16 + r0 + 8 * u;
+            if (r < n_nodes) p.ml[base + sh.nodes[r]] = make_float2(M[u], sh.bad ? -1.f : L[u]);
         }
     }
-    if (wk == 0) {
-        const size_t base = ((size_t)b * p.slots_per_b + p.slot0[h] + slot) * p.N;
-        const bool bad = sh.bad != 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (node[u] < 0) continue;
-            if ((lane & 3) == 0) p.ml[base + node[u]] = make_float2(m[u], bad ? -1.f : l[u]);
-            float *dst = p.part + (base + node[u]) * D + c0;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2 *>(dst + i * 8) = make_float2(o[i][2 * u], o[i][2 * u + 1]);
+    if (sh.odd) {
+        // the values left out: each reaches the nodes that see its key (the
+        // probability's size does not matter to an infinity or a NaN)
+        for (int c = tid; c < D; c += kThreads)
+            for (int part = 0; part < n_parts; ++part)
+                for (int i = 0; i < parts[part].n; ++i) {
+                    const long long off = key_offset(p, parts[part], b, h, i);
+                    if (off < 0) continue;
+                    const __nv_bfloat16 *v = parts[part].kind == kNodes
+                                                 ? static_cast<const __nv_bfloat16 *>(p.node_rows) + (size_t)p.N * D
+                                                 : static_cast<const __nv_bfloat16 *>(p.cache[1]);
+                    const float x = __bfloat162float(v[off + c]);
+                    if (fabsf(x) < INFINITY) continue;
+                    for (int n = 0; n < n_nodes; ++n)
+                        if (sh.ti.depth[n] >= 0 && key_count(p, parts[part], sh.ti, h, pos, sh.ti.depth[n], sh.ti.anc[n], n, i))
+                            so[n * D + (c + 8 * (n & 15)) % D] += x;
+                }
+        __syncthreads();
+    }
+#pragma unroll 2
+    for (int e = tid; e < n_nodes * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        const float *src = so + r * D + (c + 8 * (r & 15)) % D;
+        float4 x = *reinterpret_cast<const float4 *>(src);
+        for (int k = 1; k < WK; ++k) {
+            const float4 y = *reinterpret_cast<const float4 *>(src + k * WM * 16 * D);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         }
+        *reinterpret_cast<float4 *>(p.part + (base + sh.nodes[r]) * D + c) = x;
     }
 }
 
@@ -378,33 +349,31 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) 
         return;
     }
     const int ws = p.wsplit[h];
-    if (li < ws) {
-        Keys parts[2];
-        const int n = local_keys(p, h, pos, li, parts);
-        if (li == 0) {
-            run_tree<__nv_bfloat16, D, kThreads>(p, sh.parent, b, h, reinterpret_cast<float *>(ring));
-            __threadfence();   // the copies of these rows go past L1
-        }
-        if (tid == 0) sh.n = p.N;
-        if (tid < p.N) sh.nodes[tid] = tid;
-        run_item<D, true>(p, sh, ring, parts, n, b, h, pos, p.nsplit[h] + li);
-        return;
-    }
     const int sets = tree_num_sets(p, p.dil[h], sh.ti.max_depth), items = sets * p.nsplit[h];
-    for (int x = li - ws; x < items; x += p.slab_ctas[h]) {
-        const int g = x % sets, piece = x / sets;
-        Keys ks;
-        if (!slab_keys(p, h, pos, g, piece, ks)) continue;
-        __syncthreads();
-        if (tid < 32) list_nodes(p, sh.ti, h, g, sh.nodes, &sh.n);
-        run_item<D, false>(p, sh, ring, &ks, 1, b, h, pos, piece);
+    // CTAs below ws take one local item, the others slab items x, x + slab_ctas, ...
+#pragma unroll 1
+    for (int x = li < ws ? items - 1 : li - ws; x < items; x += p.slab_ctas[h]) {
+        Keys parts[2];
+        int n = 1, slot = x / sets;
+        if (li < ws) {
+            slot = p.nsplit[h] + li;
+            n = local_keys(p, h, pos, li, parts);
+            if (li == 0) run_tree<__nv_bfloat16, D>(p, sh.parent, b, h, ring);
+            if (tid == 0) sh.n = p.N;
+            if (tid < p.N) sh.nodes[tid] = tid;
+        } else {
+            if (!slab_keys(p, h, pos, x % sets, slot, parts[0])) continue;
+            __syncthreads();
+            if (tid < 32) list_nodes(p, sh.ti, h, x % sets, sh.nodes, &sh.n);
+        }
+        run_item<D>(p, sh, ring, parts, n, b, h, pos, slot);
     }
 }
 
 template <int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
-    const size_t smem = kStages * (size_t)Shape<D>::kStage;
-    static_assert((size_t)kStages * Shape<D>::kStage >= kTreeMaxNodes * kThreads * sizeof(float), "the recurrence's history fits");
-    static_assert((size_t)kStages * Shape<D>::kStage >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
+    constexpr size_t kRing = kStages * (size_t)Shape<D>::kStage;
+    static_assert(kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
+    const size_t smem = kRing > tree_smem<D>(kTreeMaxNodes) ? kRing : tree_smem<D>(kTreeMaxNodes);
     static std::atomic<unsigned long long> smem_set{0};
     cudaError_t e = ensure_smem_limit(tree_mma_kernel<D>, smem, smem_set);
     if (e != cudaSuccess) return e;

@@ -133,7 +133,7 @@ __device__ __forceinline__ int tree_set_rows(const TreeParams &p, int h, int pos
         row0 = 0;
         return pos / D;
     }
-    const int r = (int)(((long long)pos + g) % D);
+    const int r = (int)(((unsigned)pos + g) % (unsigned)D);
     row0 = (long long)r * p.slab[h];
     return pos > r ? (pos - 1 - r) / D + 1 : 0;
 }

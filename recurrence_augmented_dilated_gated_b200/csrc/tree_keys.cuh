@@ -26,15 +26,22 @@ struct Keys {
     int n;            // keys
 };
 
+// Element offset of key i: of its cache row (-1: no valid page), or of the
+// node's row.  Rows and positions fit in 32 bits (D * ceil(cap / D) < cap + D).
 __device__ __forceinline__ long long key_offset(const TreeParams &p, const Keys &ks, int b, int h, int i) {
-    if (ks.kind == kNodes) return ((((long long)b * p.H + h) * 2) * p.N + i) * p.d;   // keys; values N * d further
-    long long row = ks.row0 + i;
+    const long long bh = (long long)b * p.H + h;
+    if (ks.kind == kNodes) return (bh * 2 * p.N + i) * p.d;   // keys; values N * d further
+    unsigned row = (unsigned)ks.row0 + i;
     if (ks.kind == kWindow) {
-        long long main_row, ring_row;
-        cache_rows_of(row, p.dil[h], p.win[h], p.slab[h], p.grid, main_row, ring_row);
-        row = ring_row >= 0 ? ring_row : main_row;
+        const unsigned j = row, D = p.dil[h], S = p.slab[h];
+        if (!p.grid) row = D == 1 ? j : j % D * S + j / D;
+        else row = D > 1 ? S + j % (unsigned)p.win[h] : j;   // the ring
     }
-    return cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H, p.d, b, h, row);
+    if (!p.page_table) return (bh * p.cache_R + row) * p.d;
+    const unsigned pi = row / (unsigned)p.page_rows, pr = row - pi * p.page_rows;
+    const int pg = p.page_table[(long long)b * p.pps + pi];
+    if (pg < 0 || pg >= p.num_pages) return -1;
+    return (((long long)pg * p.H + h) * p.page_rows + pr) * p.d;
 }
 
 // How often key i counts for a node of depth `dep` and branch `anc` (0, 1 or 2).

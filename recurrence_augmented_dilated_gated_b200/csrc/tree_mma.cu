@@ -163,6 +163,7 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
                 const uint4 x = *e;
                 if (not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w)) {
                     __nv_bfloat16 *w = reinterpret_cast<__nv_bfloat16 *>(e);
+#pragma unroll 1
                     for (int i = 0; i < 8; ++i)
                         if (!(fabsf(__bfloat162float(w[i])) < INFINITY)) w[i] = __float2bfloat16_rn(0.f);
                     sh.odd = 1;
@@ -282,7 +283,9 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
         const int r = r0 + 8 * u;
         M[u] = -INFINITY;
         L[u] = 0.f;
+#pragma unroll 1
         for (int x = 0; x < WK; ++x) M[u] = fmaxf(M[u], sh.m[x * WM + wm][r]);
+#pragma unroll 1
         for (int x = 0; x < WK; ++x) {
             const float mm = sh.m[x * WM + wm][r], ll = sh.l[x * WM + wm][r];
             L[u] += mm == -INFINITY ? ll : ll * exp2f(mm - M[u]);   // -inf: nothing seen (0), or NaN
@@ -304,8 +307,11 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
     if (sh.odd) {
         // the values left out: each reaches the nodes that see its key (the
         // probability's size does not matter to an infinity or a NaN)
+#pragma unroll 1
         for (int c = tid; c < D; c += kThreads)
+#pragma unroll 1
             for (int part = 0; part < n_parts; ++part)
+#pragma unroll 1
                 for (int i = 0; i < parts[part].n; ++i) {
                     const long long off = key_offset(p, parts[part], b, h, i);
                     if (off < 0) continue;
@@ -314,6 +320,7 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
                                                  : static_cast<const __nv_bfloat16 *>(p.cache[1]);
                     const float x = __bfloat162float(v[off + c]);
                     if (fabsf(x) < INFINITY) continue;
+#pragma unroll 1
                     for (int n = 0; n < n_nodes; ++n)
                         if (sh.ti.depth[n] >= 0 && key_count(p, parts[part], sh.ti, h, pos, sh.ti.depth[n], sh.ti.anc[n], n, i))
                             so[n * D + (c + 8 * (n & 15)) % D] += x;
@@ -325,6 +332,7 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
         const int r = e / (D / 4), c = (e % (D / 4)) * 4;
         const float *src = so + r * D + (c + 8 * (r & 15)) % D;
         float4 x = *reinterpret_cast<const float4 *>(src);
+#pragma unroll 1
         for (int k = 1; k < WK; ++k) {
             const float4 y = *reinterpret_cast<const float4 *>(src + k * WM * 16 * D);
             x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;

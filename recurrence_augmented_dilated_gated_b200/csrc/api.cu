@@ -127,8 +127,8 @@ rat_status check_tree(const rat_cfg *c, int cap) {
     if (c->T > kTreeMaxNodes) return fail(RAT_ERR_UNSUPPORTED, "T = %d exceeds %d nodes", c->T, kTreeMaxNodes);
     if (cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cap);
     TreeParams p;
-    tree_plan(c, cap, &p);
-    const long long most = std::max((long long)p.ctas_per_b, (long long)c->H * c->T);
+    tree_plan(c, cap, 0, &p);
+    const long long most = std::max((long long)std::max(p.ctas_per_b, p.slots_per_b), (long long)c->H * c->T);
     if ((double)c->B * (double)most >= 2147483647.0)
         return fail(RAT_ERR_UNSUPPORTED, "B = %d entries are too many for one tree step", c->B);
     return RAT_OK;
@@ -176,7 +176,7 @@ Layout layout(const rat_cfg *c, int op, int cap) {
     if (op == RAT_OP_TREE) {
         TreeParams tmp;
         L.tree = off;
-        off = align256(off + tree_plan(c, cap, &tmp).total);
+        off = align256(off + tree_plan(c, cap, 0, &tmp).total);
     }
     L.total = off;
     return L;
@@ -865,7 +865,7 @@ rat_status tree_step(const rat_cfg *cfg_in, const void *q, const void *k, const 
     if (st != RAT_OK) return st;
     TreeParams p;
     memset(&p, 0, sizeof(p));
-    const TreeLayout tl = tree_plan(&c, cache_cap, &p);
+    const TreeLayout tl = tree_plan(&c, cache_cap, pc ? pc->page_rows : 0, &p);
     p.q = q; p.k = k; p.v = v; p.g = g;
     p.parent = parent;
     p.state[0] = state_k; p.state[1] = state_v;

@@ -334,7 +334,12 @@ template <typename T, int D, int MQ> cudaError_t launch_simt(const TreeParams &p
 
 template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
     const unsigned grid = (unsigned)p.B * (unsigned)p.ctas_per_b;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
+    if (p.n_tc > 0) {
+        e = launch_tree_tc(p, s);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+    }
     if constexpr (sizeof(T) == 2) e = launch_tree_mma(p, grid, s);
     else e = p.N <= 16 ? launch_simt<T, D, 16>(p, grid, s) : launch_simt<T, D, 64>(p, grid, s);
     if (e != cudaSuccess) return e;
@@ -350,7 +355,8 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, cudaS
 // further (down to kRowsMin) only while the batch's items would leave SMs idle.
 // How many of a head's D slabs a tree touches is known on the device only (its
 // depth): kSetsGuess CTAs per piece share them, and loop when there are more.
-TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p) {
+TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
+    constexpr int kTcMinNodes = 16;
     constexpr int kRowsMax = 4096, kRowsMin = 256, kItemsWanted = 4 * 148, kSetsGuess = 8;
     const bool grid = (c->flags & RAT_FLAG_GRID_DILATION) != 0;
     const int N = c->T;
@@ -369,6 +375,7 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p) {
     // kItemsWanted * 4 in all, however many items there are.
     long long share = c->B > 0 ? (4ll * kItemsWanted + (long long)c->B * c->H - 1) / ((long long)c->B * c->H) : 1;
     int ctas = 0, slots = 0, per_head = 0;
+    p->n_tc = p->tc_items_per_b = 0;
     long long R = 0;
     for (int h = 0; h < c->H; ++h) {
         const int D = c->dil[h];
@@ -383,6 +390,13 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p) {
         p->wsplit[h] = w > target ? (w + target - 1) / target : 1;
         const long long most = (long long)sets_of(D) * ns;
         p->slab_ctas[h] = (int)(most < share ? most : share);
+        if (c->dtype == RAT_BF16 && c->d == 128 && (grid || D == 1) && N > kTcMinNodes &&
+            tree_tc_pages(page_rows)) {
+            p->slab_ctas[h] = 0;
+            p->tc_head[p->n_tc] = (unsigned char)h;
+            p->tc_item0[p->n_tc++] = p->tc_items_per_b;
+            p->tc_items_per_b += ns;
+        }
         p->cta0[h] = ctas;
         p->slot0[h] = slots;
         p->recur[h] = (c->recur == nullptr || c->recur[h] != 0) ? 1 : 0;

@@ -37,6 +37,10 @@ struct TreeParams {
     int cta0[kMaxHeads + 1];     // first CTA of head h within an entry
     int slot0[kMaxHeads + 1];    // first partial slot of head h within an entry
     unsigned char recur[kMaxHeads];
+    // heads whose held rows tree_tc.cu takes (slab_ctas is 0), and their pieces
+    int n_tc, tc_items_per_b;
+    unsigned char tc_head[kMaxHeads];
+    int tc_item0[kMaxHeads + 1];
     WsHeader *hdr;
 };
 
@@ -137,12 +141,12 @@ __device__ __forceinline__ int tree_set_rows(const TreeParams &p, int h, int pos
     row0 = (long long)r * p.slab[h];
     return pos > r ? (pos - 1 - r) / D + 1 : 0;
 }
-// How n rows are cut: at most `most` pieces of equal length, none shorter than
-// kTreeMinRows (but the last).
+// How n rows are cut: at most `most` pieces of equal length, in whole 128 rows
+// (but the last).
 constexpr int kTreeMinRows = 128;
 __device__ __forceinline__ int tree_piece_rows(int n, int most) {
     const int pieces = max(1, min(most, (n + kTreeMinRows - 1) / kTreeMinRows));
-    return ((n + pieces - 1) / pieces + 15) & ~15;
+    return ((n + pieces - 1) / pieces + 127) & ~127;   // whole tiles, and whole pages of 128 rows or a divisor
 }
 
 // Gate of one channel: a = sigmoid(g) and 1 - a without cancellation, as in the
@@ -158,11 +162,15 @@ __device__ __forceinline__ void gate_pair(float g, float &a, float &oma) {
 struct TreeLayout {
     size_t node_rows, part, ml, total;
 };
-TreeLayout tree_plan(const rat_cfg *c, int cap, TreeParams *p);
+TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p);
 
 cudaError_t launch_tree(const TreeParams &p, int dtype, cudaStream_t s);
 // the attention part of a bf16 step (tree_mma.cu)
 cudaError_t launch_tree_mma(const TreeParams &p, unsigned grid, cudaStream_t s);
+// the held rows of its heads in tc_head (tree_tc.cu), and whether pages of
+// page_rows rows suit its copies (0: a dense cache)
+bool tree_tc_pages(int page_rows);
+cudaError_t launch_tree_tc(const TreeParams &p, cudaStream_t s);
 
 // Commit of the accepted branch (tree_commit.cu).
 struct CommitParams {

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) 
     const int sets = tree_num_sets(p, p.dil[h], sh.ti.max_depth), items = sets * p.nsplit[h];
     // CTAs below ws take one local item, the others slab items x, x + slab_ctas, ...
 #pragma unroll 1
-    for (int x = li < ws ? items - 1 : li - ws; x < items; x += p.slab_ctas[h]) {
+    for (int x = li < ws ? items - 1 : li - ws; x < items; x += max(1, p.slab_ctas[h])) {
         Keys parts[2];
         int n = 1, slot = x / sets;
         if (li < ws) {

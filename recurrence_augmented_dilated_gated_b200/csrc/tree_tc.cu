@@ -1,0 +1,505 @@
+// tree_tc.cu -- K7 for heads whose nodes all read the same rows (D = 1, or the
+// fixed grid) and whose tree is large: the held rows on the 5th-generation
+// tensor cores (tcgen05 + TMEM), bf16 operands, d = 128.
+//
+// The products are taken transposed, so that the 128 rows of an instruction are
+// always full however many nodes N a tree has:
+//   S^T [128 keys x N] = K~ Q^T      (A = the K~ tile, B = the nodes' queries)
+//   O^T [128 channels x N] += V~^T P^T   (A = the V~ tile read along its rows)
+// A thread of the softmax warps owns one key (a TMEM lane) and all its scores;
+// the reference a node's scores are measured from is shared by all keys and
+// raised, for the whole CTA, only when a score passes it by more than 2^8.  The
+// sums of P stay in registers, a node's share of each key, and are added
+// across the CTA once per item.
+//
+// One persistent CTA per SM walks over items (runs of rows of one (b, h)):
+//   warps 0-3  softmax: S^T from TMEM, P^T (bf16) to shared memory, at an item's
+//              end O^T from TMEM to the item's partial; they also stage the next
+//              item's queries once its last scores are in
+//   warp 4     copies: K~ and V~ tiles (32 KB each) into a ring of six slots, by
+//              TMA, 128-byte swizzled; a page is a box of its own.  (16-byte
+//              asynchronous copies by two warps instead, for any page size, took
+//              3.3 TB/s at N = 32.)
+//   warp 5     TMEM owner; one lane issues the instructions: the scores of tile
+//              t + 1 before the product of tile t, so that one runs during the
+//              softmax of the other
+// TMEM: S0 [0,64) S1 [64,128) O [128,192) columns.
+// Bound: HBM.  128 rows take 64 KB, 2830 cycles of an SM's share of the memory
+// bandwidth, against 512 of the tensor core and about 700 of the softmax at
+// N = 64.
+//
+// Every wait is bounded (globaltimer); on expiry the CTA records
+// RAT_ERR_TIMEOUT, drains its copies and instructions, frees its TMEM, exits.
+#include "attn_tc.cuh"
+#include "tmem_io.cuh"
+#include "tree_keys.cuh"
+
+namespace rat {
+
+namespace {
+
+constexpr int kSoftmax = 128;
+constexpr int kThreads = kSoftmax + 64;
+constexpr int kD = 128;
+constexpr int kTile = 128;               // keys per tile
+constexpr int kSlots = 6;
+constexpr uint32_t kHalf = kTile * 128;  // 64 channels of a tile: rows of 128 bytes
+constexpr uint32_t kSlot = 2 * kHalf;    // a K~ or a V~ tile
+constexpr uint32_t kQHalf = kTreeMaxNodes * 128;
+constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
+constexpr int kTmemCols = 256;
+constexpr float kSlack = 8.f;            // log2 of how far P may pass 1
+constexpr long long kWaitNs = 2000000000LL;
+
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// False when the wait gave up or another role has.
+__device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    const unsigned long long t0 = global_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if ((long long)(global_ns() - t0) > kWaitNs) return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// Shared-memory matrix descriptor: 128-byte swizzle, groups of eight 128-byte
+// lines 1024 bytes apart; `lbo` is the distance of 64-element blocks for an
+// operand that is contiguous along its rows (M or N), unused otherwise.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, fp32 accumulation, bf16 operands, M = 128; `mn`: both operands are
+// contiguous along M / N instead of along K.
+__device__ __forceinline__ uint32_t idesc(int N, bool mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The items of a CTA, in order; every role walks the same list.
+struct Items {
+    int u, b, h, slot, tiles;
+    Keys ks;
+    __device__ __forceinline__ bool next(const TreeParams &p, int total) {
+        for (;; ) {
+            u += gridDim.x;
+            if (u >= total) return false;
+            b = u / p.tc_items_per_b;
+            const int it = u % p.tc_items_per_b;
+            int lo = 0, hi = p.n_tc - 1;   // largest i with tc_item0[i] <= it
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.tc_item0[mid] <= it) lo = mid; else hi = mid - 1;
+            }
+            h = p.tc_head[lo];
+            slot = it - p.tc_item0[lo];
+            const int pos = p.pos[b];
+            if (pos < 0 || pos > p.cap || !slab_keys(p, h, pos, 0, slot, ks)) continue;
+            tiles = (ks.n + kTile - 1) / kTile;
+            return true;
+        }
+    }
+};
+
+struct Shared {
+    uint64_t full[kSlots], empty[kSlots], sfull[2], sempty[2], qfull, pfull, pvdone, copied[4], soft, drain;
+    uint32_t tmem;
+    volatile int abort;
+    int bad[4];                       // item number + 1 of an item with an invalid page, by item mod 4 (the copies
+                                      // run at most three items ahead of the softmax, as does copied)
+    volatile int over[2];             // tile number + 1 when a reference has to be raised, by tile mod 2
+    alignas(16) float ref[kTreeMaxNodes];   // read four at a time
+    float corr[kTreeMaxNodes];
+    float part[4][kTreeMaxNodes];     // a warp's maxima or sums
+};
+
+struct Maps {
+    CUtensorMap kv[2];
+    int box;             // rows of a box: a tile, or a page that is shorter
+};
+
+template <int NP>   // nodes, padded to 32 or 64
+__global__ void __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int total = p.B * p.tc_items_per_b;
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.sempty[i], kSoftmax);
+        }
+        mbar_init(&sh.qfull, kSoftmax);
+        mbar_init(&sh.pfull, kSoftmax);
+        mbar_init(&sh.pvdone, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.copied[i], 32);
+        mbar_init(&sh.soft, kSoftmax);
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        for (int i = 0; i < 4; ++i) sh.bad[i] = 0;
+        sh.over[0] = sh.over[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sh.tmem, base = smem_u32(smem);
+    Items it;
+    it.u = (int)blockIdx.x - (int)gridDim.x;
+    bool ok = true;
+
+    if (warp == 5) {
+        // ------------------------------------------------ instruction issue
+        if (lane == 0) {
+            int j = 0, t_all = 0, items = 0, pv_slot = -1;   // ring slots and tiles so far; slot of a V~ tile not yet multiplied
+            bool pv_first = false;
+            const uint32_t iqk = idesc(NP, false), ipv = idesc(NP, true);
+            auto product = [&](int t) {   // O^T += V~^T P^T of tile t
+                const int s = pv_slot % kSlots;
+                if (!mbar_wait(&sh.full[s], (pv_slot / kSlots) & 1, &sh.abort) || !mbar_wait(&sh.pfull, t & 1, &sh.abort)) return false;
+                tc_after();
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    tc_mma(tmem + 128, sdesc(base + s * kSlot + k * 2048, kHalf), sdesc(base + kOffP + k * 2048, 16), ipv, k > 0 || !pv_first);
+                tc_commit(&sh.empty[s]);
+                tc_commit(&sh.pvdone);
+                return true;
+            };
+            while (ok && it.next(p, total)) {
+                ok = mbar_wait(&sh.qfull, items & 1, &sh.abort);
+                ++items;
+                for (int t = 0; ok && t < it.tiles; ++t, ++t_all) {
+                    const int s = j % kSlots;
+                    ok = mbar_wait(&sh.full[s], (j / kSlots) & 1, &sh.abort) &&
+                         (t_all < 2 || mbar_wait(&sh.sempty[t_all & 1], (t_all / 2 - 1) & 1, &sh.abort));
+                    if (!ok) break;
+                    tc_after();
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k)
+                        tc_mma(tmem + (t_all & 1) * 64, sdesc(base + s * kSlot + (k >> 2) * kHalf + (k & 3) * 32, 16),
+                               sdesc(base + kOffQ + (k >> 2) * kQHalf + (k & 3) * 32, 16), iqk, k > 0);
+                    tc_commit(&sh.empty[s]);
+                    tc_commit(&sh.sfull[t_all & 1]);
+                    if (pv_slot >= 0) ok = product(t_all - 1);
+                    pv_slot = j + 1;
+                    pv_first = t == 0;
+                    j += 2;
+                }
+            }
+            if (ok && pv_slot >= 0) ok = product(t_all - 1);
+            if (!ok) {
+                sh.abort = 1;
+                report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
+            }
+            tc_commit(&sh.drain);   // everything issued has finished before TMEM is freed
+            volatile int never = 0;
+            mbar_wait(&sh.drain, 0, &never);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------ copies
+        // lane 2 i + x brings half x (64 channels) of box i of a tile
+        const int half = lane & 1, first = (lane >> 1) * maps.box;
+        int j = 0, items = 0;
+        while (ok && it.next(p, total)) {
+            bool bad = false;
+            for (int t = 0; ok && t < it.tiles; ++t) {
+                const unsigned row = (unsigned)it.ks.row0 + t * kTile + first;
+                int y = (int)row, z = it.b * p.H + it.h;
+                bool on = first < kTile && t * kTile + first < it.ks.n;
+                if (on && p.page_table) {
+                    const unsigned pi = row / (unsigned)p.page_rows;
+                    const int pg = p.page_table[(long long)it.b * p.pps + pi];
+                    y = (int)(row - pi * p.page_rows);
+                    z = pg * p.H + it.h;
+                    if (pg < 0 || pg >= p.num_pages) {
+                        bad = true;
+                        on = false;
+                    }
+                }
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, on)) * maps.box * 128;
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x, ++j) {
+                    const int s = j % kSlots;
+                    if (j >= kSlots) ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[s], (j / kSlots - 1) & 1, &sh.abort));
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect(&sh.full[s], bytes);
+                    __syncwarp();
+                    if (on) tma_load(base + s * kSlot + half * kHalf + first * 128, &maps.kv[x], &sh.full[s], half * 64, y, z);
+                }
+            }
+            if (bad) sh.bad[items & 3] = items + 1;
+            mbar_arrive(&sh.copied[items & 3]);
+            ++items;
+        }
+        if (!ok) {
+            sh.abort = 1;
+            if (lane == 0) report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
+            volatile int never = 0;
+            for (int q = max(0, j - kSlots); q < j; ++q)   // copies still in flight
+                mbar_wait(&sh.full[q % kSlots], (q / kSlots) & 1, &never);
+        }
+    } else {
+        // ------------------------------------------------ softmax
+        const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+        int t_all = 0, items = 0, syncs = 0;
+        // all softmax warps (a bounded wait, so that a warp that gave up strands no other)
+        auto sync = [&]() {
+            mbar_arrive(&sh.soft);
+            return __all_sync(0xffffffffu, mbar_wait(&sh.soft, syncs++ & 1, &sh.abort)) != 0;
+        };
+        // queries of an item: row n of Q is node n (absent nodes: zeros)
+        auto stage_q = [&](int b, int h) {
+            for (int e = tid; e < NP * 16; e += kSoftmax) {
+                const int n = e >> 4, c = e & 15;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (n < p.N && p.parent[(size_t)b * p.N + n] != RAT_NODE_ABSENT)
+                    x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (((size_t)b * p.N + n) * p.H + h) * kD + c * 8);
+                *reinterpret_cast<uint4 *>(smem + kOffQ + (c >> 3) * kQHalf + n * 128 + (((c & 7) ^ (n & 7)) << 4)) = x;
+            }
+            fence_async();
+            mbar_arrive(&sh.qfull);
+        };
+        bool more = it.next(p, total);
+        if (more) stage_q(it.b, it.h);
+        while (ok && more) {
+            float l[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) l[n] = 0.f;
+            for (int t = 0; t < it.tiles; ++t, ++t_all) {
+                ok = mbar_wait(&sh.sfull[t_all & 1], (t_all / 2) & 1, &sh.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_after();
+                uint32_t s[NP];
+#pragma unroll
+                for (int n = 0; n < NP; n += 32) tmem_ld32(t_lane + (t_all & 1) * 64 + n, s + n);
+                tc_before();
+                mbar_arrive(&sh.sempty[t_all & 1]);
+                const bool valid = t * kTile + tid < it.ks.n;
+                bool over = t == 0;
+                if (!over) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < NP; n += 4) {
+                        const float4 r = *reinterpret_cast<const float4 *>(&sh.ref[n]);
+                        mx = fmaxf(mx, fmaxf(fmaxf(fmaf(__uint_as_float(s[n]), p.scale_log2, -r.x), fmaf(__uint_as_float(s[n + 1]), p.scale_log2, -r.y)),
+                                             fmaxf(fmaf(__uint_as_float(s[n + 2]), p.scale_log2, -r.z), fmaf(__uint_as_float(s[n + 3]), p.scale_log2, -r.w))));
+                    }
+                    over = valid && mx > kSlack;
+                }
+                if (over) sh.over[t_all & 1] = t_all + 1;
+                if (!(ok = sync())) break;
+                if (sh.over[t_all & 1] == t_all + 1) {
+                    // some reference is raised (the first tile sets all of them):
+                    // maxima over the tile's keys, by the integers in the floats' order
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) {
+                        const float x = __uint_as_float(s[n]) * p.scale_log2;
+                        int i = __float_as_int(valid && x == x ? x : -INFINITY);
+                        i ^= (i >> 31) & 0x7fffffff;
+                        i = __reduce_max_sync(0xffffffffu, i);
+                        i ^= (i >> 31) & 0x7fffffff;
+                        if (lane == (n & 31)) sh.part[warp][n] = __int_as_float(i);
+                    }
+                    if (!(ok = sync())) break;
+                    if (tid < NP) {
+                        float mx = fmaxf(fmaxf(sh.part[0][tid], sh.part[1][tid]), fmaxf(sh.part[2][tid], sh.part[3][tid]));
+                        if (mx == -INFINITY) mx = 0.f;   // nothing but scores of -inf: they weigh nothing
+                        const float old = sh.ref[tid];
+                        const bool up = t == 0 || mx > old + kSlack;
+                        sh.corr[tid] = t > 0 && up ? exp2f(old - mx) : 1.f;
+                        if (up) sh.ref[tid] = mx;
+                    }
+                    if (!(ok = sync())) break;
+                    if (t > 0) {
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) l[n] *= sh.corr[n];
+                        ok = mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_after();
+#pragma unroll 1
+                        for (int n = 0; n < NP; n += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(t_lane + 128 + n, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.corr[n + i]);
+                            tmem_st32(t_lane + 128 + n, o);
+                        }
+                        tc_before();
+                    }
+                }
+                if (t_all > 0) {   // P of the tile before has been read
+                    ok = mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+                uint8_t *row = smem + kOffP + tid * 128;
+#pragma unroll
+                for (int n = 0; n < NP; n += 8) {
+                    const float4 ra = *reinterpret_cast<const float4 *>(&sh.ref[n]), rb = *reinterpret_cast<const float4 *>(&sh.ref[n + 4]);
+                    const float r[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        float a = ex2(fmaf(__uint_as_float(s[n + i]), p.scale_log2, -r[i]));
+                        float c = ex2(fmaf(__uint_as_float(s[n + i + 1]), p.scale_log2, -r[i + 1]));
+                        if (!valid) a = c = 0.f;
+                        l[n + i] += a;
+                        l[n + i + 1] += c;
+                        __nv_bfloat162 v = __floats2bfloat162_rn(a, c);
+                        pk[i / 2] = *reinterpret_cast<uint32_t *>(&v);
+                    }
+                    *reinterpret_cast<uint4 *>(row + (((n >> 3) ^ (tid & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+                if (t == it.tiles - 1 && it.ks.n % kTile != 0) {
+                    // rows behind the item's last hold anything: their values are
+                    // zeroed, as a probability of zero does not undo a NaN
+                    const int v = 2 * t_all + 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[v % kSlots], (v / kSlots) & 1, &sh.abort));
+                    if (!ok) break;
+                    if (!valid) {
+                        uint4 *x = reinterpret_cast<uint4 *>(smem + (v % kSlots) * kSlot + tid * 128);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) x[c] = x[kHalf / 16 + c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_async();
+                mbar_arrive(&sh.pfull);
+            }
+            if (!ok) break;
+            // the item's last scores are in, so Q is free: the next item's go there
+            const int b = it.b, h = it.h, slot = it.slot;
+            more = it.next(p, total);
+            if (more) stage_q(it.b, it.h);
+            // sums over the keys: halves of the nodes change lanes until a lane
+            // holds NP / 32 nodes' sums over its warp
+#pragma unroll
+            for (int half = NP / 2, off = 16; off > 0; half >>= 1, off >>= 1) {
+                const bool up = lane & off;
+#pragma unroll
+                for (int n = 0; n < half; ++n) {
+                    const float give = up ? l[n] : l[n + half], keep = up ? l[n + half] : l[n];
+                    l[n] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                }
+            }
+            // lane bits, highest first, chose the halves: lane i holds nodes i * NP / 32 ...
+#pragma unroll
+            for (int n = 0; n < NP / 32; ++n) sh.part[warp][lane * (NP / 32) + n] = l[n];
+            if (!(ok = sync())) break;
+            const size_t rowbase = ((size_t)b * p.slots_per_b + p.slot0[h] + slot) * p.N;
+            ok = mbar_wait(&sh.copied[items & 3], (items >> 2) & 1, &sh.abort) && mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (tid < p.N) {
+                const float sum = (sh.part[0][tid] + sh.part[1][tid]) + (sh.part[2][tid] + sh.part[3][tid]);
+                const bool bad = *(volatile int *)&sh.bad[items & 3] == items + 1;
+                p.ml[rowbase + tid] = make_float2(sum == 0.f ? -INFINITY : sh.ref[tid], bad ? -1.f : sum);
+            }
+            ++items;
+            tc_after();
+#pragma unroll 1
+            for (int n = 0; n < NP; n += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_lane + 128 + n, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (n + i < p.N) p.part[(rowbase + n + i) * kD + tid] = __uint_as_float(o[i]);
+            }
+            tc_before();
+            ok = sync();   // sh.ref and sh.part are read
+        }
+        if (!ok) {
+            sh.abort = 1;
+            if (lane == 0) report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
+        }
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <int NP> cudaError_t launch_np(const TreeParams &p, cudaStream_t s) {
+    static std::atomic<unsigned long long> smem_set{0};
+    cudaError_t e = ensure_smem_limit(tree_tc_kernel<NP>, kBytes + 1024, smem_set);
+    if (e != cudaSuccess) return e;
+    Maps maps;
+    const long long rows = p.page_table ? p.page_rows : p.cache_R, blocks = (long long)(p.page_table ? p.num_pages : p.B) * p.H;
+    maps.box = p.page_table && p.page_rows < kTile ? p.page_rows : kTile;
+    for (int x = 0; x < 2; ++x)
+        if (!encode_map_rows(&maps.kv[x], p.cache[x], rows, blocks, kD, maps.box)) return cudaErrorInvalidValue;
+    const long long total = (long long)p.B * p.tc_items_per_b;
+    tree_tc_kernel<NP><<<(unsigned)(total < 148 ? total : 148), kThreads, kBytes + 1024, s>>>(p, maps);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// A page has to be a whole number of tiles or a whole part of one, in eights of
+// rows (the swizzle's period), so that a tile is a whole number of boxes.
+bool tree_tc_pages(int page_rows) {
+    return page_rows == 0 || page_rows % kTile == 0 || (page_rows % 8 == 0 && kTile % page_rows == 0);
+}
+
+cudaError_t launch_tree_tc(const TreeParams &p, cudaStream_t s) {
+    return p.N <= 32 ? launch_np<32>(p, s) : launch_np<64>(p, s);
+}
+
+}  // namespace rat

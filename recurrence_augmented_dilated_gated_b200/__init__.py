@@ -348,7 +348,7 @@ def paged_cache(cfg, pool_k, pool_v, page_table, cache_cap):
         raise ValueError("page_table must be [B, pages_per_seq]")
     desc = rat_paged_cache(pool_k.data_ptr(), pool_v.data_ptr(), page_table.data_ptr(), int(P),
                            int(page_table.shape[1]), int(n))
-    desc.device, desc.tensors = pool_k.device, (pool_k, pool_v, page_table)   # they live as long as the descriptor
+    desc.device_index, desc.tensors = pool_k.get_device(), (pool_k, pool_v, page_table)   # they live as long as the descriptor
     return desc
 
 
@@ -388,30 +388,39 @@ class _Args:
     """Arguments of one call: checked tensors of one device, on which it runs."""
 
     def __init__(self, ws):
-        if not isinstance(ws, torch.Tensor) or ws.device.type != "cuda":
+        if not isinstance(ws, torch.Tensor) or not ws.is_cuda:
             raise ValueError("ws must be a CUDA tensor (the library has no CPU path)")
-        self.device = ws.device
+        self.index = ws.get_device()
         self.ws = _ptr(ws, "ws", torch.uint8)
         self.ws_bytes = ws.numel()
 
     def ptr(self, t, name, dtype, shape, optional=False):
-        if t is not None and isinstance(t, torch.Tensor) and t.device != self.device and t.numel() > 0:
-            raise ValueError("%s is on %s, the workspace on %s" % (name, t.device, self.device))
-        return _ptr(t, name, dtype, shape, optional)
+        # the usual case in a few attribute reads: a decode step is as short as these checks
+        if (isinstance(t, torch.Tensor) and t.dtype == dtype and (shape is None or t.shape == shape)
+                and t.get_device() == self.index and t.is_contiguous()):
+            return t.data_ptr() or None
+        p = _ptr(t, name, dtype, shape, optional)
+        if t is not None and t.numel() > 0 and t.get_device() != self.index:
+            raise ValueError("%s is on %s, the workspace on cuda:%d" % (name, t.device, self.index))
+        return p
 
     def call(self, fn, what, *args, stream=None):
-        if isinstance(stream, torch.cuda.Stream) and stream.device != self.device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
-        with torch.cuda.device(self.device):
-            _check(fn(*args, self.ws, self.ws_bytes, _stream(stream)), what)
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != self.index:
+            raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, self.index))
+        if torch.cuda.current_device() == self.index:
+            rc = fn(*args, self.ws, self.ws_bytes, _stream(stream))
+        else:
+            with torch.cuda.device(self.index):
+                rc = fn(*args, self.ws, self.ws_bytes, _stream(stream))
+        _check(rc, what)
 
 
 def _paged_desc(a, cfg, cache):
     """The descriptor of a paged cache, its tensors on the call's device."""
     if not isinstance(cache, rat_paged_cache):
         raise TypeError("cache must be a rat_paged_cache (paged_cache())")
-    if getattr(cache, "device", a.device) != a.device:
-        raise ValueError("cache is on %s, the workspace on %s" % (cache.device, a.device))
+    if getattr(cache, "device_index", a.index) != a.index:
+        raise ValueError("cache is on cuda:%d, the workspace on cuda:%d" % (cache.device_index, a.index))
     return ctypes.byref(cache)
 
 

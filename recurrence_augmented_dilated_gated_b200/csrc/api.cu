@@ -120,15 +120,22 @@ rat_status check_step_cfg(const rat_cfg *c, rat_cfg *out) {
     return check_cfg(out);
 }
 
-// Sizes of a tree step or commit.  The plan's counts are bounded here, so that
-// grids and row numbers fit in 32 bits.
+// Sizes of a tree step or commit.
 rat_status check_tree(const rat_cfg *c, int cap) {
     if (c->T < 1) return fail(RAT_ERR_INVALID, "a tree needs at least one node (T = %d)", c->T);
     if (c->T > kTreeMaxNodes) return fail(RAT_ERR_UNSUPPORTED, "T = %d exceeds %d nodes", c->T, kTreeMaxNodes);
     if (cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cap);
-    TreeParams p;
-    tree_plan(c, cap, 0, &p);
-    const long long most = std::max((long long)std::max(p.ctas_per_b, p.slots_per_b), (long long)c->H * c->T);
+    if (c->B >= 0x7fffffff / 64) return fail(RAT_ERR_UNSUPPORTED, "B = %d entries are too many for one tree call", c->B);
+    return RAT_OK;
+}
+
+// The plan of a tree step; its counts are bounded here, so that grids and
+// partial slots fit in 32 bits.
+rat_status plan_tree(const rat_cfg *c, int cap, int page_rows, TreeParams *p, TreeLayout *tl) {
+    rat_status st = check_tree(c, cap);
+    if (st != RAT_OK) return st;
+    *tl = tree_plan(c, cap, page_rows, p);
+    const long long most = std::max((long long)std::max(p->ctas_per_b, p->slots_per_b), (long long)c->H * c->T);
     if ((double)c->B * (double)most >= 2147483647.0)
         return fail(RAT_ERR_UNSUPPORTED, "B = %d entries are too many for one tree step", c->B);
     return RAT_OK;
@@ -139,7 +146,6 @@ struct Layout {
     size_t lse_dil = 0, att_ticket = 0;               // attention
     size_t kt = 0, vt = 0;                            // mix scratch
     size_t part = 0;                                  // decode
-    size_t tree = 0;                                  // tree step
     int nchunks = 0, items_per_b = 0;
     size_t total = 0;
 };
@@ -173,22 +179,20 @@ Layout layout(const rat_cfg *c, int op, int cap) {
         off = align256(off + decode_plan(c, cap, &tmp));
         L.items_per_b = tmp.items_per_b;
     }
-    if (op == RAT_OP_TREE) {
-        TreeParams tmp;
-        L.tree = off;
-        off = align256(off + tree_plan(c, cap, 0, &tmp).total);
-    }
     L.total = off;
     return L;
 }
 
-rat_status check_ws(const rat_cfg *c, int op, int cap, void *ws, size_t ws_bytes, Layout *L) {
+rat_status check_ws_bytes(void *ws, size_t ws_bytes, size_t need) {
     if (!ws) return fail(RAT_ERR_INVALID, "workspace is NULL");
     if (((uintptr_t)ws & 255u) != 0) return fail(RAT_ERR_INVALID, "workspace must be 256-byte aligned");
-    *L = layout(c, op, cap);
-    if (ws_bytes < L->total)
-        return fail(RAT_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, L->total);
+    if (ws_bytes < need) return fail(RAT_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     return RAT_OK;
+}
+
+rat_status check_ws(const rat_cfg *c, int op, int cap, void *ws, size_t ws_bytes, Layout *L) {
+    *L = layout(c, op, cap);
+    return check_ws_bytes(ws, ws_bytes, L->total);
 }
 
 #define CHECK_PTR(p, name)                                                                   \
@@ -643,8 +647,10 @@ size_t rat_workspace_size(const rat_cfg *cfg, int op, int cache_cap) {
         rat_cfg tmp;
         if (check_step_cfg(cfg, &tmp) != RAT_OK) return 0;
         if (op == RAT_OP_STATUS) return sizeof(WsHeader);
-        if (check_tree(&tmp, cache_cap) != RAT_OK) return 0;
-        return layout(&tmp, op, cache_cap).total;
+        TreeParams p;
+        TreeLayout tl;
+        if (plan_tree(&tmp, cache_cap, 0, &p, &tl) != RAT_OK) return 0;
+        return sizeof(WsHeader) + tl.total;
     }
     if (check_cfg(cfg, !dec) != RAT_OK) return 0;
     if (dec && cache_cap < 1) return 0;
@@ -853,26 +859,25 @@ rat_status tree_step(const rat_cfg *cfg_in, const void *q, const void *k, const 
     rat_cfg c;
     rat_status st = check_step_cfg(cfg_in, &c);
     if (st != RAT_OK) return st;
-    st = check_tree(&c, cache_cap);
+    TreeParams p;
+    memset(&p, 0, sizeof(p));
+    TreeLayout tl;
+    st = plan_tree(&c, cache_cap, pc ? pc->page_rows : 0, &p, &tl);
     if (st != RAT_OK) return st;
     if (c.B == 0) return RAT_OK;
     CHECK_PTR(q, "q"); CHECK_PTR(k, "k"); CHECK_PTR(v, "v"); CHECK_PTR(g, "g"); CHECK_PTR(parent, "parent");
     CHECK_PTR(state_k, "state_k"); CHECK_PTR(state_v, "state_v");
     CHECK_PTR(cache_k, "cache_k"); CHECK_PTR(cache_v, "cache_v");
     CHECK_PTR(pos, "pos"); CHECK_PTR(o, "o"); CHECK_OPT(lse, "lse");
-    Layout L;
-    st = check_ws(&c, RAT_OP_TREE, cache_cap, ws, ws_bytes, &L);
+    st = check_ws_bytes(ws, ws_bytes, sizeof(WsHeader) + tl.total);
     if (st != RAT_OK) return st;
-    TreeParams p;
-    memset(&p, 0, sizeof(p));
-    const TreeLayout tl = tree_plan(&c, cache_cap, pc ? pc->page_rows : 0, &p);
     p.q = q; p.k = k; p.v = v; p.g = g;
     p.parent = parent;
     p.state[0] = state_k; p.state[1] = state_v;
     p.cache[0] = cache_k; p.cache[1] = cache_v;
     set_paged(pc, p.page_table, p.page_rows, p.pps, p.num_pages);
     p.pos = pos; p.o = o; p.lse = lse;
-    char *w = static_cast<char *>(ws) + L.tree;
+    char *w = static_cast<char *>(ws) + sizeof(WsHeader);
     p.node_rows = w + tl.node_rows;
     p.part = reinterpret_cast<float *>(w + tl.part);
     p.ml = reinterpret_cast<float2 *>(w + tl.ml);
@@ -900,8 +905,7 @@ rat_status tree_commit(const rat_cfg *cfg_in, const void *k, const void *v, cons
     CHECK_PTR(out_state_k, "out_state_k"); CHECK_PTR(out_state_v, "out_state_v");
     CHECK_PTR(cache_k, "cache_k"); CHECK_PTR(cache_v, "cache_v");
     CHECK_PTR(pos, "pos"); CHECK_PTR(out_pos, "out_pos");
-    Layout L;
-    st = check_ws(&c, RAT_OP_STATUS, 0, ws, ws_bytes, &L);
+    st = check_ws_bytes(ws, ws_bytes, sizeof(WsHeader));
     if (st != RAT_OK) return st;
     CommitParams p;
     memset(&p, 0, sizeof(p));
@@ -926,6 +930,22 @@ rat_status tree_commit(const rat_cfg *cfg_in, const void *k, const void *v, cons
     cudaError_t e = launch_tree_commit(p, c.dtype, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "tree commit launch");
     return RAT_OK;
+}
+
+// The different row layouts among the heads (and which one head h has).
+int head_classes(const rat_cfg *c, int cap, HeadClass *cls, unsigned char *cls_of) {
+    int n = 0;
+    for (int h = 0; h < c->H; ++h) {
+        HeadClass k;
+        k.D = c->dil[h];
+        k.W = grid_mode(c) && k.D > 1 ? c->win[h] : 0;
+        k.S = (int)(((long long)cap + k.D - 1) / k.D);
+        int i = 0;
+        while (i < n && (cls[i].D != k.D || cls[i].W != k.W)) ++i;
+        if (i == n) cls[n++] = k;
+        if (cls_of) cls_of[h] = (unsigned char)i;
+    }
+    return n;
 }
 
 rat_status check_paged_step(const rat_cfg *cfg, const rat_paged_cache *pc, int cap) {
@@ -993,8 +1013,7 @@ rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int pa
     if (c.B == 0) return RAT_OK;
     CHECK_PTR(page_table, "page_table"); CHECK_PTR(length, "length");
     CHECK_PTR(free_pages, "free_pages"); CHECK_PTR(n_free, "n_free");
-    Layout L;
-    st = check_ws(&c, RAT_OP_STATUS, 0, ws, ws_bytes, &L);
+    st = check_ws_bytes(ws, ws_bytes, sizeof(WsHeader));
     if (st != RAT_OK) return st;
     PageUpdateParams p;
     memset(&p, 0, sizeof(p));
@@ -1002,15 +1021,7 @@ rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int pa
     p.B = c.B; p.pps = pages_per_seq; p.page_rows = page_rows; p.num_pages = num_pages;
     p.cap = cache_cap; p.extra = extra;
     p.grid = grid_mode(&c) ? 1 : 0;
-    for (int h = 0; h < c.H; ++h) {
-        HeadClass k;
-        k.D = c.dil[h];
-        k.W = p.grid && k.D > 1 ? c.win[h] : 0;
-        k.S = (int)(((long long)cache_cap + k.D - 1) / k.D);
-        int i = 0;
-        while (i < p.ncls && (p.cls[i].D != k.D || p.cls[i].W != k.W)) ++i;
-        if (i == p.ncls) p.cls[p.ncls++] = k;
-    }
+    p.ncls = head_classes(&c, cache_cap, p.cls, nullptr);
     p.hdr = reinterpret_cast<WsHeader *>(ws);
     cudaError_t e = launch_page_update(p, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "page table launch");
@@ -1029,9 +1040,10 @@ rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int ca
     }
     if (cache_cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cache_cap);
     if (empty(&c)) return RAT_OK;
+    if ((double)c.B * c.T >= 2147483647.0 || (double)c.B * ((c.T + 31) / 32) >= 2147483647.0)
+        return fail(RAT_ERR_UNSUPPORTED, "B x T exceeds 2^31 positions");
     CHECK_PTR(pos, "pos"); CHECK_OPT(count, "count"); CHECK_PTR(slots, "slots"); CHECK_OPT(ring_slots, "ring_slots");
-    Layout L;
-    st = check_ws(&c, RAT_OP_STATUS, 0, ws, ws_bytes, &L);
+    st = check_ws_bytes(ws, ws_bytes, sizeof(WsHeader));
     if (st != RAT_OK) return st;
     SlotParams p;
     memset(&p, 0, sizeof(p));
@@ -1042,11 +1054,7 @@ rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int ca
     p.B = c.B; p.T = c.T; p.H = c.H; p.cap = cache_cap;
     p.grid = grid_mode(&c) ? 1 : 0;
     set_paged(cache, p.page_table, p.page_rows, p.pps, p.num_pages);
-    for (int h = 0; h < c.H; ++h) {
-        p.dil[h] = c.dil[h];
-        p.win[h] = c.win[h];
-        p.slab[h] = (int)(((long long)cache_cap + c.dil[h] - 1) / c.dil[h]);
-    }
+    p.ncls = head_classes(&c, cache_cap, p.cls, p.cls_of);
     p.hdr = reinterpret_cast<WsHeader *>(ws);
     cudaError_t e = launch_slot_map(p, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "slot map launch");

@@ -13,7 +13,9 @@
 // counts are summed through distributed shared memory, and a second pass over
 // the run turns ballots into ranks.
 // Bound: latency (three sweeps of a run by its warp and three cluster
-// barriers); the table itself is read from DRAM once.
+// barriers); a lane's first kHeld entries stay in registers between the sweeps
+// (8 x 32 warps x 16 x 32 entries: 256 sequences of 512 pages), and their loads
+// go out together.
 //
 // Slot map.  The row of the flat pool (or flat dense cache) that holds a
 // position of a head: index arithmetic and one table read per value, bound by
@@ -33,54 +35,71 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
 // Does a head of class c hold one of positions 0 .. n-1 in rows [p0, p1)?
-__device__ __forceinline__ bool page_needed(const HeadClass &c, int grid, long long p0, long long p1, int n) {
+// (p0 < 2^31: it is a row of the table; p1 may pass it.)
+__device__ __forceinline__ bool page_needed(const HeadClass &c, int grid, unsigned p0, long long p1, int n) {
     if (grid) {
-        if (p0 < n / c.D) return true;
+        if (p0 < (unsigned)(n / c.D)) return true;
         return c.W > 0 && p1 > c.S && p0 < (long long)c.S + min(n, c.W);
     }
     // residue r fills rows r * S .. r * S + ceil((n - r) / D) - 1 of its slab
-    const long long r = p0 / c.S;
-    if (r >= c.D) return false;
-    const long long filled = n > r ? (n - 1 - r) / c.D + 1 : 0;
+    const unsigned r = p0 / (unsigned)c.S;
+    if (r >= (unsigned)c.D) return false;
+    const unsigned filled = n > (int)r ? (unsigned)(n - 1 - (int)r) / (unsigned)c.D + 1 : 0;
     if (p0 - r * c.S < filled) return true;
-    return (r + 1) * c.S < p1 && r + 1 < c.D && r + 1 < n;   // the next slab starts inside the page
+    return (r + 1) * (long long)c.S < p1 && (int)r + 1 < c.D && (int)r + 1 < n;   // the next slab starts inside the page
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) page_update_kernel(const PageUpdateParams p) {
+constexpr int kHeld = 16;   // entries of a run that a lane keeps in registers between the sweeps
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) page_update_kernel(const PageUpdateParams p) {
     __shared__ int s_cnt[2][kWarps];       // entries of each warp that give / take a page
     __shared__ int s_sum[2];               // and of the CTA
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster.block_rank();
-    const int total = p.B * p.pps;
-    const int run = ((total + kCluster * kWarps - 1) / (kCluster * kWarps) + 31) & ~31;
-    const long long e_lo = (long long)(rank * kWarps + warp) * run;
-    const long long e_hi = min(e_lo + run, (long long)total);
+    const int total = p.B * p.pps;         // < 2^31
+    const int run = (int)((((long long)total + kCluster * kWarps - 1) / (kCluster * kWarps) + 31) & ~31LL);
+    const long long lo = (long long)(rank * kWarps + warp) * run;
+    const int e_lo = (int)min(lo, (long long)total), e_hi = (int)min(lo + run, (long long)total);
     const int n_free = *p.n_free;
     const unsigned below = (1u << lane) - 1u;
 
     // state of one entry: bit 0 has, bit 1 needed
-    auto state = [&](long long e, int &page) {
-        page = -1;
-        if (e >= e_hi) return 0;
-        const int b = (int)(e / p.pps), pi = (int)(e % p.pps);
-        page = p.table[e];
+    auto state = [&](int page, int e) {
+        const int b = (unsigned)e / (unsigned)p.pps;
         const int len = p.length[b];
         bool need = false;
         if (len >= 0 && len <= p.cap) {
             const int n = (int)min((long long)len + p.extra, (long long)p.cap);
-            const long long p0 = (long long)pi * p.page_rows;
-            for (int c = 0; c < p.ncls && !need; ++c) need = page_needed(p.cls[c], p.grid, p0, p0 + p.page_rows, n);
+            const unsigned p0 = (unsigned)(e - b * p.pps) * (unsigned)p.page_rows;
+            const long long p1 = (long long)p0 + p.page_rows;
+#pragma unroll 1
+            for (int c = 0; c < p.ncls && !need; ++c) need = page_needed(p.cls[c], p.grid, p0, p1, n);
         }
         const bool has = page >= 0 && page < p.num_pages;
         if (len > p.cap) need = has;   // a length out of range: the entry stays as it is
         return (has ? 1 : 0) | (need ? 2 : 0);
     };
 
+    // the first kHeld * 32 entries of the run: loaded together, kept with their states
+    int held[kHeld];
+    unsigned states = 0;                   // two bits each
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = e_lo + i * 32 + lane < e_hi ? p.table[e_lo + i * 32 + lane] : -1;
     int give = 0, take = 0;
-    for (long long e = e_lo; e < e_hi; e += 32) {
-        int page;
-        const int st = state(e + lane, page);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        if (e_lo + i * 32 >= e_hi) break;
+        const int e = e_lo + i * 32 + lane, st = e < e_hi ? state(held[i], e) : 0;
+        states |= (unsigned)st << (2 * i);
+        give += __popc(__ballot_sync(0xffffffffu, st == 1));
+        take += __popc(__ballot_sync(0xffffffffu, st == 2));
+    }
+    // the others are looked at again in every sweep
+    const int e_more = e_lo + kHeld * 32;
+#pragma unroll 2
+    for (int e = e_more; e < e_hi; e += 32) {
+        const int st = e + lane < e_hi ? state(p.table[e + lane], e + lane) : 0;
         give += __popc(__ballot_sync(0xffffffffu, st == 1));
         take += __popc(__ballot_sync(0xffffffffu, st == 2));
     }
@@ -116,38 +135,49 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
     // a stack that cannot be right (more pages given back than there are) is left alone
     const bool ok = n_free >= 0 && (long long)n_free + gives <= p.num_pages;
     const int top = n_free + gives;
+    auto put_back = [&](int st, int page) {
+        const unsigned m = __ballot_sync(0xffffffffu, st == 1);
+        if (st == 1) p.free_pages[n_free + give0 + __popc(m & below)] = page;
+        give0 += __popc(m);
+    };
+    auto settle = [&](int st, int e) {
+        const unsigned m = __ballot_sync(0xffffffffu, st == 2);
+        if (e < e_hi && st == 2) {
+            const int at = top - 1 - (take0 + __popc(m & below));
+            int got = at >= 0 ? __ldcg(p.free_pages + at) : -1;
+            if (at < 0) {
+                report_error(p.hdr, RAT_ERR_NO_PAGES, (int)((unsigned)e / (unsigned)p.pps));
+            } else if (got < 0 || got >= p.num_pages) {
+                got = -1;
+                report_error(p.hdr, RAT_ERR_INVALID, (int)((unsigned)e / (unsigned)p.pps));
+            }
+            p.table[e] = got;
+        } else if (e < e_hi && st != 3) {
+            p.table[e] = -1;
+        }
+        take0 += __popc(m);
+    };
     if (ok) {
-        for (long long e = e_lo; e < e_hi; e += 32) {
-            int page;
-            const int st = state(e + lane, page);
-            const unsigned m = __ballot_sync(0xffffffffu, st == 1);
-            if (st == 1) p.free_pages[n_free + give0 + __popc(m & below)] = page;
-            give0 += __popc(m);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            if (e_lo + i * 32 >= e_hi) break;
+            put_back((states >> (2 * i)) & 3, held[i]);
+        }
+#pragma unroll 1
+        for (int e = e_more; e < e_hi; e += 32) {
+            const int page = e + lane < e_hi ? p.table[e + lane] : -1;
+            put_back(e + lane < e_hi ? state(page, e + lane) : 0, page);
         }
     }
     cluster.sync();   // the pages given back are on the stack
     if (ok) {
-        for (long long e = e_lo; e < e_hi; e += 32) {
-            int page;
-            const int st = state(e + lane, page);
-            const unsigned m = __ballot_sync(0xffffffffu, st == 2);
-            if (e + lane < e_hi) {
-                if (st == 2) {
-                    const int at = top - 1 - (take0 + __popc(m & below));
-                    int got = at >= 0 ? __ldcg(p.free_pages + at) : -1;
-                    if (at < 0) {
-                        report_error(p.hdr, RAT_ERR_NO_PAGES, (int)((e + lane) / p.pps));
-                    } else if (got < 0 || got >= p.num_pages) {
-                        got = -1;
-                        report_error(p.hdr, RAT_ERR_INVALID, (int)((e + lane) / p.pps));
-                    }
-                    p.table[e + lane] = got;
-                } else if (st != 3) {
-                    p.table[e + lane] = -1;
-                }
-            }
-            take0 += __popc(m);
+#pragma unroll 4
+        for (int i = 0; i < kHeld; ++i) {
+            if (e_lo + i * 32 >= e_hi) break;
+            settle((states >> (2 * i)) & 3, e_lo + i * 32 + lane);
         }
+#pragma unroll 1
+        for (int e = e_more; e < e_hi; e += 32) settle(e + lane < e_hi ? state(p.table[e + lane], e + lane) : 0, e + lane);
         for (int b = rank * kThreads + tid; b < p.B; b += kCluster * kThreads)
             if (p.length[b] > p.cap) report_error(p.hdr, RAT_ERR_INVALID, b);
     }
@@ -159,27 +189,59 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
 }
 
 constexpr int kSlotThreads = 256;
+constexpr int kSlotTokens = 32;   // positions of one CTA: kSlotTokens * H values
+constexpr int kSlotClasses = 64;  // row layouts handled at a time
 
+// Heads with the same layout have a position in the same page and line, so that
+// is found once per (position, layout); a head's value is then one addition.
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams p) {
-    const long long n = (long long)p.B * p.T * p.H;
-    for (long long e = (long long)blockIdx.x * kSlotThreads + threadIdx.x; e < n; e += (long long)gridDim.x * kSlotThreads) {
-        const int h = (int)(e % p.H);
-        const long long bt = e / p.H;
-        const int i = (int)(bt % p.T), b = (int)(bt / p.T);
-        const int pos = p.pos[b], cnt = p.count ? p.count[b] : p.T;
-        const bool ok = pos >= 0 && cnt >= 0 && cnt <= p.T && (long long)pos + cnt <= p.cap;
-        if (!ok && i == 0 && h == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
-        long long row[2] = {-1, -1};
-        if (ok && i < cnt) {
-            cache_rows_of((long long)pos + i, p.dil[h], p.win[h], p.slab[h], p.grid, row[0], row[1]);
-            if (i < cnt - p.win[h]) row[1] = -1;   // a later position of the run takes the ring row
+    __shared__ long long s_at[2][kSlotTokens * kSlotClasses];   // place of head 0's row (-1: none)
+    __shared__ unsigned char s_cls[kMaxHeads];
+    const int tid = threadIdx.x;
+    const int chunks = (p.T + kSlotTokens - 1) / kSlotTokens;
+    const int b = blockIdx.x / chunks, i0 = (blockIdx.x % chunks) * kSlotTokens;
+    const int nt = min(kSlotTokens, p.T - i0);
+    const int pos = p.pos[b], cnt = p.count ? p.count[b] : p.T;
+    const bool ok = pos >= 0 && cnt >= 0 && cnt <= p.T && pos <= p.cap && cnt <= p.cap - pos;
+    if (!ok && i0 == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
+    for (int h = tid; h < p.H; h += kSlotThreads) s_cls[h] = p.cls_of[h];
+    // place of logical row `row` of head 0; a head further is `stride` rows on
+    const long long stride = p.page_table ? p.page_rows : p.cache_R;
+    auto place = [&](unsigned row) -> long long {
+        if (!p.page_table) return (long long)b * p.H * p.cache_R + row;
+        const unsigned pi = row / (unsigned)p.page_rows;
+        const int pg = p.page_table[(long long)b * p.pps + pi];
+        if (pg < 0 || pg >= p.num_pages) return -1;
+        return (long long)pg * p.H * p.page_rows + (row - pi * p.page_rows);
+    };
+    for (int c0 = 0; c0 < p.ncls; c0 += kSlotClasses) {
+        const int nc = min(kSlotClasses, p.ncls - c0);
+        __syncthreads();
+        for (int e = tid; e < nt * nc; e += kSlotThreads) {
+            const int i = i0 + e / nc, c = e % nc;
+            const HeadClass &k = p.cls[c0 + c];
+            long long main_at = -1, ring_at = -1;
+            if (ok && i < cnt) {
+                const unsigned j = (unsigned)pos + i, q = j / (unsigned)k.D, r = j - q * k.D;
+                if (!p.grid) main_at = place(r * k.S + q);
+                else if (r == (unsigned)k.D - 1) main_at = place(q);
+                // the ring's row, unless a later position of the run takes it
+                if (p.ring && k.W > 0 && i >= cnt - k.W) ring_at = place(k.S + j % (unsigned)k.W);
+            }
+            s_at[0][e] = main_at;
+            s_at[1][e] = ring_at;
         }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            long long *out = w ? p.ring : p.slots;
-            if (!out) continue;
-            // the offset of channel 0 in a cache of one channel is the row
-            out[e] = row[w] < 0 ? -1 : cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H, 1, b, h, row[w]);
+        __syncthreads();
+        const size_t out0 = ((size_t)b * p.T + i0) * p.H;
+        for (int e = tid; e < nt * p.H; e += kSlotThreads) {
+            const int i = e / p.H, h = e - i * p.H, c = s_cls[h] - c0;
+            if (c < 0 || c >= nc) continue;
+            const long long m = s_at[0][i * nc + c];
+            p.slots[out0 + e] = m < 0 ? -1 : m + h * stride;
+            if (p.ring) {
+                const long long r = s_at[1][i * nc + c];
+                p.ring[out0 + e] = r < 0 ? -1 : r + h * stride;
+            }
         }
     }
 }
@@ -193,9 +255,8 @@ cudaError_t launch_page_update(const PageUpdateParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_slot_map(const SlotParams &p, cudaStream_t s) {
-    const long long n = (long long)p.B * p.T * p.H;
-    if (n == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)min((n + kSlotThreads - 1) / kSlotThreads, 148ll * 16);
+    if ((long long)p.B * p.T == 0) return cudaSuccess;
+    const unsigned grid = (unsigned)p.B * (unsigned)((p.T + kSlotTokens - 1) / kSlotTokens);
     slot_map_kernel<<<grid, kSlotThreads, 0, s>>>(p);
     count_launches(1);
     return cudaGetLastError();

@@ -30,9 +30,9 @@ struct SlotParams {
     int B, T, H, cap, grid;
     const int *page_table;
     int page_rows, pps, num_pages;
-    int dil[kMaxHeads];
-    int win[kMaxHeads];
-    int slab[kMaxHeads];
+    int ncls;                    // W of a class: the ring's length, 0 without one
+    HeadClass cls[kMaxHeads];
+    unsigned char cls_of[kMaxHeads];
     WsHeader *hdr;
 };
 cudaError_t launch_slot_map(const SlotParams &p, cudaStream_t s);

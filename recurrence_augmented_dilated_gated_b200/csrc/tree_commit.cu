@@ -10,8 +10,10 @@
 //
 // A cluster of kCluster CTAs serves one entry, so that pos can be advanced in
 // place: every CTA reads pos[b] before the cluster's barrier and one writes it
-// after.  A thread owns four channels of one head and tensor and walks the
-// branch, its loads issued kAhead nodes at a time.
+// after.  A thread owns four channels of one head, keys and values (one gate
+// for both), and walks the branch with the loads of kAhead nodes in flight; it
+// steps row numbers along instead of dividing.  512 threads an entry keep the
+// whole of a batch of 256 (16 heads x 128) resident at once.
 // Bound: latency of the walk at small batches, bytes (k, v, g of the branch
 // read, its rows written, the states both) at large ones.
 #include <cooperative_groups.h>
@@ -22,31 +24,45 @@ namespace rat {
 
 namespace {
 
-constexpr int kCluster = 8;
-constexpr int kThreads = 256;
+constexpr int kCluster = 4;
+constexpr int kThreads = 128;
 constexpr int kAhead = 4;
+
+__device__ __forceinline__ void step4(float4 &s, const float4 &x, const float4 &a, const float4 &oma) {
+    s.x = a.x * s.x + oma.x * x.x;
+    s.y = a.y * s.y + oma.y * x.y;
+    s.z = a.z * s.z + oma.z * x.z;
+    s.w = a.w * s.w + oma.w * x.w;
+}
+__device__ __forceinline__ void gate4(const float4 &g, float4 &a, float4 &oma) {
+    gate_pair(g.x, a.x, oma.x);
+    gate_pair(g.y, a.y, oma.y);
+    gate_pair(g.z, a.z, oma.z);
+    gate_pair(g.w, a.w, oma.w);
+}
 
 template <typename T>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tree_commit_kernel(const CommitParams p) {
-    __shared__ int s_path[kTreeMaxNodes];
+    __shared__ int s_parent[kTreeMaxNodes], s_path[kTreeMaxNodes];
     __shared__ int s_len;
     const int tid = threadIdx.x;
     const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
     const int N = p.N;
-    const int *parent = p.parent + (size_t)b * N;
     const int pos = p.pos[b], leaf = p.leaf[b];
+    if (tid < N) s_parent[tid] = p.parent[(size_t)b * N + tid];
+    __syncthreads();
     if (tid == 0) {
         // the branch, leaf first; a parent is below its child's index, so the
         // walk ends.  -1: an argument out of range
         int n = 0, i = leaf;
         bool ok = pos >= 0 && pos <= p.cap && leaf >= -1 && leaf < N;
         while (ok && i >= 0) {
-            const int up = parent[i];
+            const int up = s_parent[i];
             ok = up >= -1 && up < i;
             s_path[n++] = i;
             i = up;
         }
-        ok = ok && pos + n <= p.cap;
+        ok = ok && pos <= p.cap - n;
         s_len = ok ? n : -1;
     }
     __syncthreads();
@@ -64,53 +80,64 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
             if (r1 >= 0)
                 bad |= cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H, p.d, b, h, r1) < 0;
         }
+        bad = __syncthreads_or(bad);
     }
-    bad = __syncthreads_or(bad);
     if (bad) {
         len = 0;
         if (tid == 0 && rank == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
     }
-    const int vec = p.d / 4, units = p.H * 2 * vec;
+    const int vec = p.d / 4, units = p.H * vec;
+    const T *kin = static_cast<const T *>(p.k), *vin = static_cast<const T *>(p.v), *gin = static_cast<const T *>(p.g);
+    const T *gvin = gin + (p.sep ? (size_t)p.B * N * p.H * p.d : 0);
+    T *ck = static_cast<T *>(p.cache[0]), *cv = static_cast<T *>(p.cache[1]);
     for (int u = rank * kThreads + tid; u < units; u += kCluster * kThreads) {
-        const int c = (u % vec) * 4, hx = u / vec, x = hx & 1, h = hx >> 1;
+        const int c = (u % vec) * 4, h = u / vec;
         const size_t e0 = ((size_t)b * p.H + h) * p.d + c;
-        const T *src = static_cast<const T *>(x ? p.v : p.k);
-        const T *gate = static_cast<const T *>(p.g) + (p.sep && x ? (size_t)p.B * N * p.H * p.d : 0);
-        T *cache = static_cast<T *>(p.cache[x]);
         const bool rec = p.recur[h] != 0;
-        float4 s = *reinterpret_cast<const float4 *>(p.state[x] + e0);
+        float4 sk = *reinterpret_cast<const float4 *>(p.state[0] + e0), sv = *reinterpret_cast<const float4 *>(p.state[1] + e0);
+        const unsigned D = p.dil[h], S = p.slab[h], W = p.grid && D > 1 ? p.win[h] : 0;
+        unsigned res = (unsigned)pos % D, quo = (unsigned)pos / D, ring = W ? (unsigned)pos % W : 0;
+        auto put = [&](unsigned row) {
+            const long long off = cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H, p.d, b, h, row) + c;
+            IO4<T>::store(ck + off, sk);
+            IO4<T>::store(cv + off, sv);
+        };
         for (int i0 = 0; i0 < len; i0 += kAhead) {
-            float4 xs[kAhead], gs[kAhead];
+            float4 xk[kAhead], xv[kAhead], g[kAhead], gv[kAhead];
 #pragma unroll
             for (int w = 0; w < kAhead; ++w) {
                 if (i0 + w >= len) break;
                 const size_t e = (((size_t)b * N + s_path[len - 1 - i0 - w]) * p.H + h) * p.d + c;
-                xs[w] = IO4<T>::load(src + e);
-                if (rec) gs[w] = IO4<T>::load(gate + e);
+                xk[w] = IO4<T>::load(kin + e);
+                xv[w] = IO4<T>::load(vin + e);
+                if (rec) g[w] = IO4<T>::load(gin + e);
+                if (rec && p.sep) gv[w] = IO4<T>::load(gvin + e);
             }
 #pragma unroll
             for (int w = 0; w < kAhead; ++w) {
                 if (i0 + w >= len) break;
-                float a, oma;
                 if (rec) {
-                    gate_pair(gs[w].x, a, oma); s.x = a * s.x + oma * xs[w].x;
-                    gate_pair(gs[w].y, a, oma); s.y = a * s.y + oma * xs[w].y;
-                    gate_pair(gs[w].z, a, oma); s.z = a * s.z + oma * xs[w].z;
-                    gate_pair(gs[w].w, a, oma); s.w = a * s.w + oma * xs[w].w;
+                    float4 a, oma;
+                    gate4(g[w], a, oma);
+                    step4(sk, xk[w], a, oma);
+                    if (p.sep) gate4(gv[w], a, oma);
+                    step4(sv, xv[w], a, oma);
                 } else {
-                    s = xs[w];
+                    sk = xk[w];
+                    sv = xv[w];
                 }
-                long long r0, r1;
-                cache_rows_of((long long)pos + i0 + w, p.dil[h], p.win[h], p.slab[h], p.grid, r0, r1);
-                if (r0 >= 0)
-                    IO4<T>::store(cache + cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H,
-                                                       p.d, b, h, r0) + c, s);
-                if (r1 >= 0)   // a branch longer than the window wraps around the ring: the last position stays
-                    IO4<T>::store(cache + cache_offset(p.page_table, p.pps, p.page_rows, p.num_pages, p.cache_R, p.H,
-                                                       p.d, b, h, r1) + c, s);
+                if (!p.grid) put(res * S + quo);
+                else if (res == D - 1) put(quo);
+                if (W) put(S + ring);   // a branch longer than the window wraps around: the last position stays
+                if (++res == D) {
+                    res = 0;
+                    ++quo;
+                }
+                if (++ring == W) ring = 0;
             }
         }
-        *reinterpret_cast<float4 *>(p.out_state[x] + e0) = s;
+        *reinterpret_cast<float4 *>(p.out_state[0] + e0) = sk;
+        *reinterpret_cast<float4 *>(p.out_state[1] + e0) = sv;
     }
     cooperative_groups::this_cluster().sync();   // every CTA of the entry has read pos[b]
     if (rank == 0 && tid == 0) p.out_pos[b] = pos + len;

@@ -881,6 +881,7 @@ rat_status tree_step(const rat_cfg *cfg_in, const void *q, const void *k, const 
     p.node_rows = w + tl.node_rows;
     p.part = reinterpret_cast<float *>(w + tl.part);
     p.ml = reinterpret_cast<float2 *>(w + tl.ml);
+    p.info = reinterpret_cast<int *>(w + tl.info);
     p.cap = cache_cap; p.B = c.B; p.N = c.T; p.H = c.H; p.d = c.d;
     p.scale_log2 = scale_of(&c) * 1.4426950408889634f;
     p.hdr = reinterpret_cast<WsHeader *>(ws);
@@ -942,7 +943,12 @@ int head_classes(const rat_cfg *c, int cap, HeadClass *cls, unsigned char *cls_o
         k.S = (int)(((long long)cap + k.D - 1) / k.D);
         int i = 0;
         while (i < n && (cls[i].D != k.D || cls[i].W != k.W)) ++i;
-        if (i == n) cls[n++] = k;
+        if (i == n) {
+            k.by_d.set(k.D);
+            k.by_s.set(k.S);
+            k.by_w.set(k.W > 0 ? k.W : 1);
+            cls[n++] = k;
+        }
         if (cls_of) cls_of[h] = (unsigned char)i;
     }
     return n;
@@ -1008,8 +1014,8 @@ rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int pa
     const long long R = cache_rows(&c, cache_cap);
     if ((long long)pages_per_seq * page_rows < R)
         return fail(RAT_ERR_INVALID, "pages_per_seq x page_rows < %lld cache rows", R);
-    if ((long long)c.B * pages_per_seq >= 0x7fffffffLL)
-        return fail(RAT_ERR_UNSUPPORTED, "B x pages_per_seq exceeds 2^31 entries");
+    if ((long long)c.B * pages_per_seq >= 0x7fffffffLL || (long long)pages_per_seq * page_rows >= 0x7fffffffLL)
+        return fail(RAT_ERR_UNSUPPORTED, "B x pages_per_seq entries or pages_per_seq x page_rows rows exceed 2^31");
     if (c.B == 0) return RAT_OK;
     CHECK_PTR(page_table, "page_table"); CHECK_PTR(length, "length");
     CHECK_PTR(free_pages, "free_pages"); CHECK_PTR(n_free, "n_free");
@@ -1021,6 +1027,7 @@ rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int pa
     p.B = c.B; p.pps = pages_per_seq; p.page_rows = page_rows; p.num_pages = num_pages;
     p.cap = cache_cap; p.extra = extra;
     p.grid = grid_mode(&c) ? 1 : 0;
+    p.by_pps.set(pages_per_seq);
     p.ncls = head_classes(&c, cache_cap, p.cls, nullptr);
     p.hdr = reinterpret_cast<WsHeader *>(ws);
     cudaError_t e = launch_page_update(p, (cudaStream_t)stream);
@@ -1042,6 +1049,7 @@ rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int ca
     if (empty(&c)) return RAT_OK;
     if ((double)c.B * c.T >= 2147483647.0 || (double)c.B * ((c.T + 31) / 32) >= 2147483647.0)
         return fail(RAT_ERR_UNSUPPORTED, "B x T exceeds 2^31 positions");
+    if (cache_rows(&c, cache_cap) >= 0x7fffffffLL) return fail(RAT_ERR_UNSUPPORTED, "cache rows exceed 2^31");
     CHECK_PTR(pos, "pos"); CHECK_OPT(count, "count"); CHECK_PTR(slots, "slots"); CHECK_OPT(ring_slots, "ring_slots");
     st = check_ws_bytes(ws, ws_bytes, sizeof(WsHeader));
     if (st != RAT_OK) return st;
@@ -1054,6 +1062,8 @@ rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int ca
     p.B = c.B; p.T = c.T; p.H = c.H; p.cap = cache_cap;
     p.grid = grid_mode(&c) ? 1 : 0;
     set_paged(cache, p.page_table, p.page_rows, p.pps, p.num_pages);
+    p.by_page.set(cache ? cache->page_rows : 1);
+    p.by_h.set(c.H);
     p.ncls = head_classes(&c, cache_cap, p.cls, p.cls_of);
     p.hdr = reinterpret_cast<WsHeader *>(ws);
     cudaError_t e = launch_slot_map(p, (cudaStream_t)stream);

@@ -38,13 +38,13 @@ constexpr int kWarps = kThreads / 32;
 // (p0 < 2^31: it is a row of the table; p1 may pass it.)
 __device__ __forceinline__ bool page_needed(const HeadClass &c, int grid, unsigned p0, long long p1, int n) {
     if (grid) {
-        if (p0 < (unsigned)(n / c.D)) return true;
+        if (p0 < c.by_d.div(n)) return true;
         return c.W > 0 && p1 > c.S && p0 < (long long)c.S + min(n, c.W);
     }
     // residue r fills rows r * S .. r * S + ceil((n - r) / D) - 1 of its slab
-    const unsigned r = p0 / (unsigned)c.S;
+    const unsigned r = c.by_s.div(p0);
     if (r >= (unsigned)c.D) return false;
-    const unsigned filled = n > (int)r ? (unsigned)(n - 1 - (int)r) / (unsigned)c.D + 1 : 0;
+    const unsigned filled = n > (int)r ? c.by_d.div(n - 1 - (int)r) + 1 : 0;
     if (p0 - r * c.S < filled) return true;
     return (r + 1) * (long long)c.S < p1 && (int)r + 1 < c.D && (int)r + 1 < n;   // the next slab starts inside the page
 }
@@ -65,9 +65,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
     const unsigned below = (1u << lane) - 1u;
 
     // state of one entry: bit 0 has, bit 1 needed
-    auto state = [&](int page, int e) {
-        const int b = (unsigned)e / (unsigned)p.pps;
-        const int len = p.length[b];
+    auto state = [&](int page, int e, int len) {
+        const int b = p.by_pps.div(e);
         bool need = false;
         if (len >= 0 && len <= p.cap) {
             const int n = (int)min((long long)len + p.extra, (long long)p.cap);
@@ -82,24 +81,33 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
     };
 
     // the first kHeld * 32 entries of the run: loaded together, kept with their states
-    int held[kHeld];
+    int held[kHeld], lens[kHeld];
     unsigned states = 0;                   // two bits each
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = e_lo + i * 32 + lane < e_hi ? p.table[e_lo + i * 32 + lane] : -1;
+    for (int i = 0; i < kHeld; ++i) {
+        const int e = e_lo + i * 32 + lane;
+        held[i] = e < e_hi ? p.table[e] : -1;
+        lens[i] = e < e_hi ? p.length[p.by_pps.div(e)] : -1;
+    }
     int give = 0, take = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         if (e_lo + i * 32 >= e_hi) break;
-        const int e = e_lo + i * 32 + lane, st = e < e_hi ? state(held[i], e) : 0;
+        const int e = e_lo + i * 32 + lane, st = e < e_hi ? state(held[i], e, lens[i]) : 0;
         states |= (unsigned)st << (2 * i);
         give += __popc(__ballot_sync(0xffffffffu, st == 1));
         take += __popc(__ballot_sync(0xffffffffu, st == 2));
     }
     // the others are looked at again in every sweep
+    auto look = [&](int e, int &page) {
+        page = p.table[e];
+        return state(page, e, p.length[p.by_pps.div(e)]);
+    };
+    int page;
     const int e_more = e_lo + kHeld * 32;
 #pragma unroll 2
     for (int e = e_more; e < e_hi; e += 32) {
-        const int st = e + lane < e_hi ? state(p.table[e + lane], e + lane) : 0;
+        const int st = e + lane < e_hi ? look(e + lane, page) : 0;
         give += __popc(__ballot_sync(0xffffffffu, st == 1));
         take += __popc(__ballot_sync(0xffffffffu, st == 2));
     }
@@ -146,10 +154,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
             const int at = top - 1 - (take0 + __popc(m & below));
             int got = at >= 0 ? __ldcg(p.free_pages + at) : -1;
             if (at < 0) {
-                report_error(p.hdr, RAT_ERR_NO_PAGES, (int)((unsigned)e / (unsigned)p.pps));
+                report_error(p.hdr, RAT_ERR_NO_PAGES, (int)p.by_pps.div(e));
             } else if (got < 0 || got >= p.num_pages) {
                 got = -1;
-                report_error(p.hdr, RAT_ERR_INVALID, (int)((unsigned)e / (unsigned)p.pps));
+                report_error(p.hdr, RAT_ERR_INVALID, (int)p.by_pps.div(e));
             }
             p.table[e] = got;
         } else if (e < e_hi && st != 3) {
@@ -165,8 +173,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
         }
 #pragma unroll 1
         for (int e = e_more; e < e_hi; e += 32) {
-            const int page = e + lane < e_hi ? p.table[e + lane] : -1;
-            put_back(e + lane < e_hi ? state(page, e + lane) : 0, page);
+            const int st = e + lane < e_hi ? look(e + lane, page) : 0;
+            put_back(st, page);
         }
     }
     cluster.sync();   // the pages given back are on the stack
@@ -177,7 +185,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
             settle((states >> (2 * i)) & 3, e_lo + i * 32 + lane);
         }
 #pragma unroll 1
-        for (int e = e_more; e < e_hi; e += 32) settle(e + lane < e_hi ? state(p.table[e + lane], e + lane) : 0, e + lane);
+        for (int e = e_more; e < e_hi; e += 32) settle(e + lane < e_hi ? look(e + lane, page) : 0, e + lane);
         for (int b = rank * kThreads + tid; b < p.B; b += kCluster * kThreads)
             if (p.length[b] > p.cap) report_error(p.hdr, RAT_ERR_INVALID, b);
     }
@@ -189,18 +197,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
 }
 
 constexpr int kSlotThreads = 256;
-constexpr int kSlotTokens = 32;   // positions of one CTA: kSlotTokens * H values
+constexpr int kSlotPlaces = 2048; // places (position, row layout) of a CTA, at a time
 constexpr int kSlotClasses = 64;  // row layouts handled at a time
+// positions of one CTA: as many as the places allow, between 32 and 128 (32 for
+// any number of layouts took 30 us for 8.2 M values: the CTAs' first loads,
+// nine waves of them, were the time)
+int slot_tokens(int ncls) { return ncls <= 16 ? 128 : ncls <= 32 ? 64 : 32; }
 
 // Heads with the same layout have a position in the same page and line, so that
 // is found once per (position, layout); a head's value is then one addition.
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams p) {
-    __shared__ long long s_at[2][kSlotTokens * kSlotClasses];   // place of head 0's row (-1: none)
+    __shared__ long long s_at[2][kSlotPlaces];   // place of head 0's row (-1: none)
     __shared__ unsigned char s_cls[kMaxHeads];
     const int tid = threadIdx.x;
-    const int chunks = (p.T + kSlotTokens - 1) / kSlotTokens;
-    const int b = blockIdx.x / chunks, i0 = (blockIdx.x % chunks) * kSlotTokens;
-    const int nt = min(kSlotTokens, p.T - i0);
+    const int chunks = (p.T + p.tokens - 1) / p.tokens;
+    const int b = blockIdx.x / chunks, i0 = (blockIdx.x % chunks) * p.tokens;
+    const int nt = min(p.tokens, p.T - i0);
     const int pos = p.pos[b], cnt = p.count ? p.count[b] : p.T;
     const bool ok = pos >= 0 && cnt >= 0 && cnt <= p.T && pos <= p.cap && cnt <= p.cap - pos;
     if (!ok && i0 == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
@@ -209,7 +221,7 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
     const long long stride = p.page_table ? p.page_rows : p.cache_R;
     auto place = [&](unsigned row) -> long long {
         if (!p.page_table) return (long long)b * p.H * p.cache_R + row;
-        const unsigned pi = row / (unsigned)p.page_rows;
+        const unsigned pi = p.by_page.div(row);
         const int pg = p.page_table[(long long)b * p.pps + pi];
         if (pg < 0 || pg >= p.num_pages) return -1;
         return (long long)pg * p.H * p.page_rows + (row - pi * p.page_rows);
@@ -222,11 +234,11 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
             const HeadClass &k = p.cls[c0 + c];
             long long main_at = -1, ring_at = -1;
             if (ok && i < cnt) {
-                const unsigned j = (unsigned)pos + i, q = j / (unsigned)k.D, r = j - q * k.D;
+                const unsigned j = (unsigned)pos + i, q = k.by_d.div(j), r = j - q * k.D;
                 if (!p.grid) main_at = place(r * k.S + q);
                 else if (r == (unsigned)k.D - 1) main_at = place(q);
                 // the ring's row, unless a later position of the run takes it
-                if (p.ring && k.W > 0 && i >= cnt - k.W) ring_at = place(k.S + j % (unsigned)k.W);
+                if (p.ring && k.W > 0 && i >= cnt - k.W) ring_at = place(k.S + (j - k.by_w.div(j) * k.W));
             }
             s_at[0][e] = main_at;
             s_at[1][e] = ring_at;
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
         __syncthreads();
         const size_t out0 = ((size_t)b * p.T + i0) * p.H;
         for (int e = tid; e < nt * p.H; e += kSlotThreads) {
-            const int i = e / p.H, h = e - i * p.H, c = s_cls[h] - c0;
+            const int i = p.by_h.div(e), h = e - i * p.H, c = s_cls[h] - c0;
             if (c < 0 || c >= nc) continue;
             const long long m = s_at[0][i * nc + c];
             p.slots[out0 + e] = m < 0 ? -1 : m + h * stride;
@@ -256,8 +268,10 @@ cudaError_t launch_page_update(const PageUpdateParams &p, cudaStream_t s) {
 
 cudaError_t launch_slot_map(const SlotParams &p, cudaStream_t s) {
     if ((long long)p.B * p.T == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)p.B * (unsigned)((p.T + kSlotTokens - 1) / kSlotTokens);
-    slot_map_kernel<<<grid, kSlotThreads, 0, s>>>(p);
+    SlotParams q = p;
+    q.tokens = slot_tokens(p.ncls);
+    const unsigned grid = (unsigned)p.B * (unsigned)((p.T + q.tokens - 1) / q.tokens);
+    slot_map_kernel<<<grid, kSlotThreads, 0, s>>>(q);
     count_launches(1);
     return cudaGetLastError();
 }

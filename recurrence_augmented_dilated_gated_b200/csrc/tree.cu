@@ -221,12 +221,14 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeParams p)
     __shared__ int s_n, s_flags[2];   // a page was not valid; a value of the tile is not finite
     __shared__ float s_corr[kTreeMaxNodes];
     const int tid = threadIdx.x;
+    allow_next();
     const int b = blockIdx.x / p.ctas_per_b, it = blockIdx.x % p.ctas_per_b;
     const int h = find_tree_head(p, it), li = it - p.cta0[h];
     const int pos = p.pos[b];
     if (tid < 32) tree_analyse(ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
     if (tid < kTreeMaxNodes) s_parent[tid] = tid < p.N ? p.parent[(size_t)b * p.N + tid] : -2;
     __syncthreads();
+    if (li == 0) tell_pieces(p, ti, b, h, pos);
     if (!ti.valid || ti.max_depth < 0) {
         if (!ti.valid && li == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
         return;
@@ -255,72 +257,61 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeParams p)
     }
 }
 
-// Joins the partials of a node: pieces of its dilated set, then the window's
-// pieces, in that order.  One CTA takes kCombineNodes nodes of one (b, h).
-constexpr int kCombineNodes = 8;
+// Joins the partials of a node, pieces of its dilated set and then the window's,
+// in that order: a warp a node, a lane the maximum and sum of one piece and then
+// D / 32 channels of all of them.
 constexpr int kCombineThreads = 128;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeParams p) {
-    __shared__ TreeInfo ti;
-    __shared__ int s_pieces[kTreeMaxNodes];   // pieces of set g, by depth
-    const int tid = threadIdx.x;
-    const int nb = (p.N + kCombineNodes - 1) / kCombineNodes;
-    const int bh = blockIdx.x / nb, n0 = (blockIdx.x % nb) * kCombineNodes;
+    constexpr int kNodes = kCombineThreads / 32, kC = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nb = (p.N + kNodes - 1) / kNodes;
+    const int bh = blockIdx.x / nb, i = (blockIdx.x % nb) * kNodes + warp;
     const int b = bh / p.H, h = bh % p.H;
-    const int pos = p.pos[b];
-    if (tid < 32) tree_analyse(ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
-    __syncthreads();
     const int S = p.nsplit[h], ws = p.wsplit[h];
     const size_t base = ((size_t)b * p.slots_per_b + p.slot0[h]) * p.N;
+    wait_previous();
     int bad = 0;
-    if (ti.valid && ti.max_depth >= 0) {
-        if (tid < p.N) {
-            int np = 0;
-            if (ti.depth[tid] >= 0) {
-                long long row0;
-                const int n = tree_set_rows(p, h, pos, tree_set_of(p, p.dil[h], ti.depth[tid]), row0);
-                const int len = tree_piece_rows(n, S);
-                np = n == 0 ? 0 : (n + len - 1) / len;
-            }
-            s_pieces[tid] = np;
-        }
-        __syncthreads();
+    if (p.page_table) {
         // a page that was not valid anywhere in (b, h): the whole pair is skipped
-        for (int e = tid; e < (S + ws) * p.N; e += kCombineThreads) {
-            const int s = e / p.N, i = e % p.N;
-            if (ti.depth[i] >= 0 && (s >= S || s < s_pieces[i])) bad |= p.ml[base + e].y < 0.f;
+        for (int e = threadIdx.x; e < (S + ws) * p.N; e += kCombineThreads) {
+            const int s = e / p.N, np = p.info[(size_t)bh * p.N + e % p.N];
+            if (np >= 0 && (s >= S || s < np)) bad |= p.ml[base + e].y < 0.f;
+        }
+        bad = __syncthreads_or(bad);
+        if (bad && threadIdx.x == 0 && i == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
+    }
+    if (i >= p.N) return;
+    const int np = p.info[(size_t)bh * p.N + i];
+    float M = -INFINITY, L = 0.f, o[kC] = {};
+    if (np >= 0 && !bad) {
+        const int n = np + ws;   // piece x is slot x, or S + x - np past the set's
+        for (int x = lane; x < n; x += 32) M = fmaxf(M, p.ml[base + (size_t)(x < np ? x : S + x - np) * p.N + i].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 2
+        for (int x = 0; x < n; ++x) {
+            const size_t at = base + (size_t)(x < np ? x : S + x - np) * p.N + i;
+            const float2 ml = p.ml[at];
+            float a[kC];
+            if (kC == 4) *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(p.part + at * D + lane * kC);
+            else *reinterpret_cast<float2 *>(a) = *reinterpret_cast<const float2 *>(p.part + at * D + lane * kC);
+            const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);   // a sum that is NaN makes the node NaN
+            L += ml.y * w;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) o[c] += ml.y == 0.f ? 0.f : a[c] * w;
         }
     }
-    bad = __syncthreads_or(bad);
-    if (bad && tid == 0 && n0 == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
-    const bool skip = bad || !ti.valid;
-    constexpr int kVec = D / 4;
-    for (int e = tid; e < kCombineNodes * kVec; e += kCombineThreads) {
-        const int i = n0 + e / kVec, c = (e % kVec) * 4;
-        if (i >= p.N) continue;
-        float M = -INFINITY, L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!skip && ti.depth[i] >= 0) {
-            const int np = s_pieces[i];
-            for (int s = 0; s < S + ws; ++s)
-                if (s >= S || s < np) M = fmaxf(M, p.ml[base + (size_t)s * p.N + i].x);
-            for (int s = 0; s < S + ws; ++s) {
-                if (s < S && s >= np) continue;
-                const float2 ml = p.ml[base + (size_t)s * p.N + i];
-                if (ml.y == 0.f) continue;
-                const float w = exp2f(ml.x - M);
-                const float4 a = *reinterpret_cast<const float4 *>(p.part + (base + (size_t)s * p.N + i) * D + c);
-                L += ml.y * w;
-                o.x += a.x * w; o.y += a.y * w; o.z += a.z * w; o.w += a.w * w;
-            }
-            const float inv = L == 0.f ? 0.f : 1.f / L;   // a sum that is NaN makes the node NaN
-            o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-        }
-        IO4<T>::store(static_cast<T *>(p.o) + (((size_t)b * p.N + i) * p.H + h) * D + c, o);
-        if (p.lse && c == 0)
-            p.lse[(size_t)bh * p.N + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    T *dst = static_cast<T *>(p.o) + (((size_t)b * p.N + i) * p.H + h) * D + lane * kC;
+    if (kC == 4) {
+        IO4<T>::store(dst, make_float4(o[0] * inv, o[1] * inv, o[kC - 2] * inv, o[kC - 1] * inv));
+    } else {
+        store1(dst, o[0] * inv);
+        store1(dst + 1, o[1] * inv);
     }
+    if (p.lse && lane == 0) p.lse[(size_t)bh * p.N + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 template <typename T, int D, int MQ> cudaError_t launch_simt(const TreeParams &p, unsigned grid, cudaStream_t s) {
@@ -328,8 +319,7 @@ template <typename T, int D, int MQ> cudaError_t launch_simt(const TreeParams &p
     static std::atomic<unsigned long long> smem_set{0};
     cudaError_t e = ensure_smem_limit(tree_simt_kernel<T, D, MQ>, smem, smem_set);
     if (e != cudaSuccess) return e;
-    tree_simt_kernel<T, D, MQ><<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(tree_simt_kernel<T, D, MQ>, grid, kThreads, smem, s, false, p);
 }
 
 template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, cudaStream_t s) {
@@ -343,10 +333,11 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, cudaS
     if constexpr (sizeof(T) == 2) e = launch_tree_mma(p, grid, s);
     else e = p.N <= 16 ? launch_simt<T, D, 16>(p, grid, s) : launch_simt<T, D, 64>(p, grid, s);
     if (e != cudaSuccess) return e;
-    const unsigned nb = (p.N + kCombineNodes - 1) / kCombineNodes;
-    tree_combine_kernel<T, D><<<(unsigned)p.B * p.H * nb, kCombineThreads, 0, s>>>(p);
+    const unsigned nb = (p.N + kCombineThreads / 32 - 1) / (kCombineThreads / 32);
+    e = launch_after(tree_combine_kernel<T, D>, (unsigned)p.B * p.H * nb, kCombineThreads, 0, s, true, p);
+    if (e != cudaSuccess) return e;
     count_launches(2);
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -422,7 +413,8 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     L.node_rows = 0;
     L.part = al((size_t)c->B * c->H * 2 * N * c->d * elt);
     L.ml = L.part + al((size_t)c->B * slots * N * c->d * sizeof(float));
-    L.total = L.ml + al((size_t)c->B * slots * N * sizeof(float2));
+    L.info = L.ml + al((size_t)c->B * slots * N * sizeof(float2));
+    L.total = L.info + al((size_t)c->B * c->H * N * sizeof(int));
     return L;
 }
 

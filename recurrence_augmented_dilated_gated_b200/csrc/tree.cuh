@@ -20,6 +20,7 @@ struct TreeParams {
     void *node_rows;             // [B][H][2][N][d] augmented rows of the nodes (cfg dtype)
     float *part;                 // [B][slots_per_b][N][d] unnormalised accumulators
     float2 *ml;                  // [B][slots_per_b][N] (max, sum); sum < 0: a page was not valid
+    int *info;                   // [B][H][N] pieces of the node's dilated set; -1: absent, or entry skipped
     long long cache_R;
     int cap, B, N, H, d;
     int grid, dedupe, sep;       // as in DecodeParams
@@ -160,7 +161,7 @@ __device__ __forceinline__ void gate_pair(float g, float &a, float &oma) {
 // Split plan and workspace offsets of a tree step (host); returns the bytes the
 // step needs after the workspace header.
 struct TreeLayout {
-    size_t node_rows, part, ml, total;
+    size_t node_rows, part, ml, info, total;
 };
 TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p);
 

@@ -8,12 +8,11 @@
 // kept for this: the branch is walked again from the tokens, which is less
 // than storing every node's state.
 //
-// A cluster of kCluster CTAs serves one entry, so that pos can be advanced in
-// place: every CTA reads pos[b] before the cluster's barrier and one writes it
+// A cluster of up to kMaxCluster CTAs serves one entry (as many as its channels
+// fill), so that pos can be advanced in place: every CTA reads pos[b] before the cluster's barrier and one writes it
 // after.  A thread owns four channels of one head, keys and values (one gate
 // for both), and walks the branch with the loads of kAhead nodes in flight; it
-// steps row numbers along instead of dividing.  512 threads an entry keep the
-// whole of a batch of 256 (16 heads x 128) resident at once.
+// steps row numbers along instead of dividing.
 // Bound: latency of the walk at small batches, bytes (k, v, g of the branch
 // read, its rows written, the states both) at large ones.
 #include <cooperative_groups.h>
@@ -24,7 +23,7 @@ namespace rat {
 
 namespace {
 
-constexpr int kCluster = 4;
+constexpr int kMaxCluster = 8;   // portable
 constexpr int kThreads = 128;
 constexpr int kAhead = 4;
 
@@ -42,11 +41,13 @@ __device__ __forceinline__ void gate4(const float4 &g, float4 &a, float4 &oma) {
 }
 
 template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tree_commit_kernel(const CommitParams p) {
+__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParams p) {
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int kCluster = (int)cluster.num_blocks();
     __shared__ int s_parent[kTreeMaxNodes], s_path[kTreeMaxNodes];
     __shared__ int s_len;
     const int tid = threadIdx.x;
-    const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+    const int b = blockIdx.x / kCluster, rank = (int)cluster.block_rank();
     const int N = p.N;
     const int pos = p.pos[b], leaf = p.leaf[b];
     if (tid < N) s_parent[tid] = p.parent[(size_t)b * N + tid];
@@ -139,7 +140,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
         *reinterpret_cast<float4 *>(p.out_state[0] + e0) = sk;
         *reinterpret_cast<float4 *>(p.out_state[1] + e0) = sv;
     }
-    cooperative_groups::this_cluster().sync();   // every CTA of the entry has read pos[b]
+    cluster.sync();   // every CTA of the entry has read pos[b]
     if (rank == 0 && tid == 0) p.out_pos[b] = pos + len;
 }
 
@@ -147,9 +148,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tre
 
 cudaError_t launch_tree_commit(const CommitParams &p, int dtype, cudaStream_t s) {
     if (p.B == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)p.B * kCluster;
-    if (dtype == RAT_BF16) tree_commit_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else tree_commit_kernel<float><<<grid, kThreads, 0, s>>>(p);
+    const int need = (p.H * (p.d / 4) + kThreads - 1) / kThreads;
+    int size = 1;
+    while (size < need && size < kMaxCluster) size *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.B * size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = dtype == RAT_BF16 ? cudaLaunchKernelEx(&cfg, tree_commit_kernel<__nv_bfloat16>, p)
+                                      : cudaLaunchKernelEx(&cfg, tree_commit_kernel<float>, p);
+    if (e != cudaSuccess) return e;
     count_launches(1);
     return cudaGetLastError();
 }

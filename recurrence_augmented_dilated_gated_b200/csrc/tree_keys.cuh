@@ -92,6 +92,39 @@ __device__ __forceinline__ bool slab_keys(const TreeParams &p, int h, int pos, i
     return true;
 }
 
+// What tree_combine_kernel needs to know of the tree (item 0 of every head).
+__device__ __forceinline__ void tell_pieces(const TreeParams &p, const TreeInfo &ti, int b, int h, int pos) {
+    const int i = threadIdx.x;
+    if (i >= p.N) return;
+    int np = -1;
+    if (ti.valid && ti.depth[i] >= 0) {
+        long long row0;
+        const int n = tree_set_rows(p, h, pos, tree_set_of(p, p.dil[h], ti.depth[i]), row0);
+        const int len = tree_piece_rows(n, p.nsplit[h]);
+        np = n == 0 ? 0 : (n + len - 1) / len;
+    }
+    p.info[((size_t)b * p.H + h) * p.N + i] = np;
+}
+
+// Programmatic dependent launch: the next kernel of the step may start once
+// every CTA of this one has; it waits itself before it reads.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, bool after, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The nodes of set g, in order (one warp).
 __device__ __forceinline__ void list_nodes(const TreeParams &p, const TreeInfo &ti, int h, int g, int *nodes, int *n) {
     const int lane = threadIdx.x & 31;

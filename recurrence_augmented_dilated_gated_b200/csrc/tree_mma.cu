@@ -346,14 +346,17 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) 
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
     const int tid = threadIdx.x;
+    allow_next();
     const int b = blockIdx.x / p.ctas_per_b, it = blockIdx.x % p.ctas_per_b;
     const int h = find_tree_head(p, it), li = it - p.cta0[h];
     const int pos = p.pos[b];
     if (tid < 32) tree_analyse(sh.ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
     else if (tid < 32 + kTreeMaxNodes) sh.parent[tid - 32] = tid - 32 < p.N ? p.parent[(size_t)b * p.N + tid - 32] : RAT_NODE_ABSENT;
     __syncthreads();
+    if (li == 0) tell_pieces(p, sh.ti, b, h, pos);
     if (!sh.ti.valid || sh.ti.max_depth < 0) {
         if (!sh.ti.valid && li == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
+        if (blockIdx.x == gridDim.x - 1) wait_previous();
         return;
     }
     const int ws = p.wsplit[h];
@@ -376,6 +379,9 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) 
         }
         run_item<D>(p, sh, ring, parts, n, b, h, pos, slot);
     }
+    // this kernel ends after the one before it (tree_tc.cu's part of the step),
+    // so that the one after, which waits for this one, has both
+    if (blockIdx.x == gridDim.x - 1) wait_previous();
 }
 
 template <int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
@@ -385,8 +391,7 @@ template <int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cu
     static std::atomic<unsigned long long> smem_set{0};
     cudaError_t e = ensure_smem_limit(tree_mma_kernel<D>, smem, smem_set);
     if (e != cudaSuccess) return e;
-    tree_mma_kernel<D><<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(tree_mma_kernel<D>, grid, kThreads, smem, s, p.n_tc > 0, p);
 }
 
 }  // namespace

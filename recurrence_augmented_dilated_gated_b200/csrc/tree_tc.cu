@@ -168,6 +168,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    allow_next();
     const int total = p.B * p.tc_items_per_b;
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {

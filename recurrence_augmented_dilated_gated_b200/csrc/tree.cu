@@ -21,6 +21,7 @@
 //     64-bit mask); a long window is cut into further items.
 // tree_combine_kernel joins the partials in a fixed order.
 // Bound: the cache rows, each read once; 4 d operations per (node, row).
+#include <stdlib.h>
 #include "tree_keys.cuh"
 
 namespace rat {
@@ -347,7 +348,7 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, cudaS
 // How many of a head's D slabs a tree touches is known on the device only (its
 // depth): kSetsGuess CTAs per piece share them, and loop when there are more.
 TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
-    constexpr int kTcMinNodes = 16;
+    const int kTcMinNodes = getenv("TCMIN") ? atoi(getenv("TCMIN")) : 16;
     constexpr int kRowsMax = 4096, kRowsMin = 256, kItemsWanted = 4 * 148, kSetsGuess = 8;
     const bool grid = (c->flags & RAT_FLAG_GRID_DILATION) != 0;
     const int N = c->T;

@@ -9,8 +9,8 @@
 // than storing every node's state.
 //
 // A cluster of up to kMaxCluster CTAs serves one entry (as many as its channels
-// fill), so that pos can be advanced in place: every CTA reads pos[b] before the cluster's barrier and one writes it
-// after.  A thread owns four channels of one head, keys and values (one gate
+// fill), so that pos can be advanced in place: every CTA reads pos[b] before
+// the cluster's barrier and one writes it after.  A thread owns four channels of one head, keys and values (one gate
 // for both), and walks the branch with the loads of kAhead nodes in flight; it
 // steps row numbers along instead of dividing.
 // Bound: latency of the walk at small batches, bytes (k, v, g of the branch

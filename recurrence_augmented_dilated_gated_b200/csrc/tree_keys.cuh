@@ -4,6 +4,7 @@
 #pragma once
 
 #include "tree.cuh"
+#include "tree_copy.cuh"
 
 namespace rat {
 
@@ -140,9 +141,6 @@ __device__ __forceinline__ void list_nodes(const TreeParams &p, const TreeInfo &
     if (lane == 0) *n = cnt;
 }
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 // 16 bytes past L1; zeros when `on` is false (the address is not read then)
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");

@@ -18,6 +18,7 @@
 //     probability; the sum of P keeps fp32): the same rounding as the prefill's.
 // Bound: HBM for small node counts (a row's 4 d bytes are used for 4 d
 // operations per node).
+#include "attn_tc.cuh"
 #include "tree_keys.cuh"
 
 namespace rat {
@@ -57,13 +58,21 @@ template <int D> struct Shape {
     static constexpr uint32_t kHalf = kTile * kRowBytes;    // K~ of a stage, then V~
     static constexpr uint32_t kStage = 2 * kHalf;
     static constexpr int kRowsAtOnce = kThreads / kChunks;  // rows that one pass of the CTA copies
-    static __device__ __forceinline__ uint32_t at(int r, int c) { return r * kRowBytes + ((c ^ (r & 7)) << 4); }
+    // 16-byte chunk c of row r: halves of 64 channels, 128-byte swizzled as TMA writes them
+    static __device__ __forceinline__ uint32_t at(int r, int c) { return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+};
+
+// TMA maps of a dense cache; a paged one is copied row by row.
+struct Maps {
+    CUtensorMap kv[2];
 };
 
 struct Shared {
     TreeInfo ti;
     int parent[kTreeMaxNodes], nodes[kTreeMaxNodes];
     int n, bad, odd;                      // odd: some local value is not finite
+    uint64_t full[kStages];               // a slab's tile has landed
+    volatile int abort;
     uint8_t count[kTreeMaxNodes][kTile];  // how often a key of a masked tile counts for a node
     float m[kWarps][16], l[kWarps][16];
 };
@@ -72,11 +81,13 @@ struct Shared {
 // sh.nodes.  One body serves slabs and local items (what differs is where a row
 // is and which tiles carry a mask): a second copy of it would only thrash the
 // instruction cache.
+// False when a wait gave up.
 template <int D>
-__device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_t *ring, const Keys *parts, int n_parts,
-                                         int b, int h, int pos, int slot) {
+__device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, Shared &sh, uint8_t *ring, const Keys *parts,
+                                         int n_parts, int b, int h, int pos, int slot, int &fills) {
     using S = Shape<D>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    fence_async();     // what was written to the ring by ordinary stores, before TMA writes there
     __syncthreads();   // sh.n and sh.nodes are set, and the ring is free
     const int n_nodes = sh.n;
     const int WM = n_nodes <= 16 ? 1 : n_nodes <= 32 ? 2 : 4, WK = kWarps / WM;
@@ -85,9 +96,12 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
     const int tiles0 = (parts[0].n + kTile - 1) / kTile;
     const int n_tiles = tiles0 + (n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0);
     if (tid == 0) sh.bad = sh.odd = 0;
+    const bool bulk = parts[0].kind == kSlab && !p.page_table;   // the item's tiles come by TMA
+    const int fill0 = fills;                                     // such tiles before this item's
+    if (bulk) fills += n_tiles;
 
     // Q into the stage that no tile uses yet
-    const uint32_t sq = smem_u32(ring) + (kStages - 1) * S::kStage;
+    const uint32_t sq = smem_u32(ring) + ((fill0 + kStages - 1) % kStages) * S::kStage;
     for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
         const int r = e / S::kChunks, c = e % S::kChunks;
         const bool on = r < n_nodes;
@@ -96,6 +110,20 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
     }
     cp_commit();
     auto load = [&](int t) {
+        if (bulk) {
+            if (tid == 0) {
+                const int f = fill0 + t, y = (int)parts[0].row0 + t * kTile;
+                uint64_t *bar = &sh.full[f % kStages];
+                const uint32_t dst = smem_u32(ring) + (f % kStages) * S::kStage;
+                mbar_expect(bar, S::kStage);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int half = 0; half < D / 64; ++half)
+                        tma_load(dst + x * S::kHalf + half * (kTile * 128), &maps.kv[x], bar, half * 64, y, b * p.H + h);
+            }
+            return;
+        }
         const bool second = t >= tiles0;
         const Keys &ks = parts[second ? 1 : 0];
         const int k0 = (second ? t - tiles0 : t) * kTile;
@@ -112,7 +140,7 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
             off = key_offset(p, ks, b, h, k0 + mine);
             if (off < 0) sh.bad = 1;
         }
-        const uint32_t dst = smem_u32(ring) + (t % kStages) * S::kStage;
+        const uint32_t dst = smem_u32(ring) + ((fill0 + t) % kStages) * S::kStage;
         const int c = lane % S::kChunks;
 #pragma unroll
         for (int i = 0; i < 16 / kPerPass; ++i) {
@@ -134,17 +162,22 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
     uint32_t q[D / 16][4];   // the warp's nodes: rows of Q as A fragments
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) ldsm4(q[k], sq + S::at(wm * 16 + (lane & 15), 2 * k + (lane >> 4)));
+    fence_async();     // Q's stage is a tile's next
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    bool ok = true;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // references, this lane's part of the sums
 
 #pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
-        cp_wait<kStages - 2>();
-        const uint32_t sk = smem_u32(ring) + (t % kStages) * S::kStage, sv = sk + S::kHalf;
+        const int f = fill0 + t;
+        uint8_t *stage = ring + (f % kStages) * S::kStage;
+        if (bulk) ok = mbar_wait(&sh.full[f % kStages], (f / kStages) & 1, &sh.abort);
+        else cp_wait<kStages - 2>();
+        const uint32_t sk = smem_u32(stage), sv = sk + S::kHalf;
         const bool second = t >= tiles0;
         const Keys &ks = parts[second ? 1 : 0];
         const int k0 = (second ? t - tiles0 : t) * kTile;
@@ -156,7 +189,7 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
             // values that are not finite leave the tile: a zero probability times
             // one of them would reach every node.  add_odd() puts them back
             __syncwarp();
-            uint4 *v = reinterpret_cast<uint4 *>(ring + (t % kStages) * S::kStage + S::kHalf);
+            uint4 *v = reinterpret_cast<uint4 *>(stage + S::kHalf);
 #pragma unroll 1
             for (int r = tid / S::kChunks; r < kTile; r += S::kRowsAtOnce) {
                 uint4 *e = v + S::at(r, tid % S::kChunks) / 16;
@@ -170,7 +203,24 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
                 }
             }
         }
-        __syncthreads();   // the tile has landed for everyone, and the one before is done with
+        if (bulk && k0 + kTile > ks.n) {
+            // rows behind the item's last hold anything: their values are zeroed
+            uint4 *v = reinterpret_cast<uint4 *>(stage + S::kHalf);
+#pragma unroll 1
+            for (int r = tid / S::kChunks; r < kTile; r += S::kRowsAtOnce)
+                if (k0 + r >= ks.n) v[S::at(r, tid % S::kChunks) / 16] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // the tile has landed for everyone, and the one before is done with
+        if (!__syncthreads_and(ok)) {
+            if (tid == 0) {
+                report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
+                volatile int never = 0;
+                for (int q = f; q < fill0 + min(n_tiles, t + kStages - 1); ++q)   // copies in flight
+                    mbar_wait(&sh.full[q % kStages], (q / kStages) & 1, &never);
+            }
+            __syncthreads();
+            return false;
+        }
         if (masked) {
 #pragma unroll 1
             for (int e = tid; e < n_nodes * kTile; e += kThreads) {
@@ -339,17 +389,25 @@ __device__ __forceinline__ void run_item(const TreeParams &p, Shared &sh, uint8_
         }
         *reinterpret_cast<float4 *>(p.part + (base + sh.nodes[r]) * D + c) = x;
     }
+    return true;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) {
-    extern __shared__ __align__(128) uint8_t ring[];
+__global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     allow_next();
     const int b = blockIdx.x / p.ctas_per_b, it = blockIdx.x % p.ctas_per_b;
     const int h = find_tree_head(p, it), li = it - p.cta0[h];
     const int pos = p.pos[b];
+    if (tid == kThreads - 1) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    int fills = 0;
     if (tid < 32) tree_analyse(sh.ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
     else if (tid < 32 + kTreeMaxNodes) sh.parent[tid - 32] = tid - 32 < p.N ? p.parent[(size_t)b * p.N + tid - 32] : RAT_NODE_ABSENT;
     __syncthreads();
@@ -377,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) 
             __syncthreads();
             if (tid < 32) list_nodes(p, sh.ti, h, x % sets, sh.nodes, &sh.n);
         }
-        run_item<D>(p, sh, ring, parts, n, b, h, pos, slot);
+        if (!run_item<D>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills)) break;
     }
     // this kernel ends after the one before it (tree_tc.cu's part of the step),
     // so that the one after, which waits for this one, has both
@@ -387,11 +445,15 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p) 
 template <int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
     constexpr size_t kRing = kStages * (size_t)Shape<D>::kStage;
     static_assert(kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
-    const size_t smem = kRing > tree_smem<D>(kTreeMaxNodes) ? kRing : tree_smem<D>(kTreeMaxNodes);
+    const size_t smem = (kRing > tree_smem<D>(kTreeMaxNodes) ? kRing : tree_smem<D>(kTreeMaxNodes)) + 1024;
     static std::atomic<unsigned long long> smem_set{0};
     cudaError_t e = ensure_smem_limit(tree_mma_kernel<D>, smem, smem_set);
     if (e != cudaSuccess) return e;
-    return launch_after(tree_mma_kernel<D>, grid, kThreads, smem, s, p.n_tc > 0, p);
+    Maps maps = {};
+    if (!p.page_table)
+        for (int x = 0; x < 2; ++x)
+            if (!encode_map_rows(&maps.kv[x], p.cache[x], p.cache_R, (long long)p.B * p.H, D, kTile)) return cudaErrorInvalidValue;
+    return launch_after(tree_mma_kernel<D>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
 }
 
 }  // namespace

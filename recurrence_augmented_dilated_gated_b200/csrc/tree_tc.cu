@@ -32,6 +32,7 @@
 // RAT_ERR_TIMEOUT, drains its copies and instructions, frees its TMEM, exits.
 #include "attn_tc.cuh"
 #include "tmem_io.cuh"
+#include "tree_copy.cuh"
 #include "tree_keys.cuh"
 
 namespace rat {
@@ -49,47 +50,7 @@ constexpr uint32_t kQHalf = kTreeMaxNodes * 128;
 constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
 constexpr int kTmemCols = 256;
 constexpr float kSlack = 8.f;            // log2 of how far P may pass 1
-constexpr long long kWaitNs = 2000000000LL;
 
-__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return ok != 0;
-}
-// False when the wait gave up or another role has.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    const unsigned long long t0 = global_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort_flag) return false;
-            if ((long long)(global_ns() - t0) > kWaitNs) return false;
-        }
-    }
-}
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
-}
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
@@ -156,12 +117,26 @@ struct Shared {
     float part[4][kTreeMaxNodes];     // a warp's maxima or sums
 };
 
+// NP columns of this thread's TMEM lane
+template <int NP> __device__ __forceinline__ void ld_cols(uint32_t addr, uint32_t *r) {
+    if constexpr (NP == 16) {
+        tmem_ld16(addr, r);
+    } else {
+#pragma unroll
+        for (int n = 0; n < NP; n += 32) tmem_ld32(addr + n, r + n);
+    }
+}
+template <int NP> __device__ __forceinline__ void st_cols(uint32_t addr, const uint32_t *r) {
+    if constexpr (NP == 16) tmem_st16(addr, r);
+    else tmem_st32(addr, r);
+}
+
 struct Maps {
     CUtensorMap kv[2];
     int box;             // rows of a box: a tile, or a page that is shorter
 };
 
-template <int NP>   // nodes, padded to 32 or 64
+template <int NP>   // nodes, padded to 16, 32 or 64
 __global__ void __launch_bounds__(kThreads, 1)
 tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t raw[];
@@ -295,6 +270,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         }
     } else {
         // ------------------------------------------------ softmax
+        constexpr int kCols = NP < 32 ? NP : 32;   // columns of O at a time
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
         int t_all = 0, items = 0, syncs = 0;
         // all softmax warps (a bounded wait, so that a warp that gave up strands no other)
@@ -326,8 +302,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                 if (!ok) break;
                 tc_after();
                 uint32_t s[NP];
-#pragma unroll
-                for (int n = 0; n < NP; n += 32) tmem_ld32(t_lane + (t_all & 1) * 64 + n, s + n);
+                ld_cols<NP>(t_lane + (t_all & 1) * 64, s);
                 tc_before();
                 mbar_arrive(&sh.sempty[t_all & 1]);
                 const bool valid = t * kTile + tid < it.ks.n;
@@ -374,12 +349,12 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                         if (!ok) break;
                         tc_after();
 #pragma unroll 1
-                        for (int n = 0; n < NP; n += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(t_lane + 128 + n, o);
+                        for (int n = 0; n < NP; n += kCols) {
+                            uint32_t o[kCols];
+                            ld_cols<kCols>(t_lane + 128 + n, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.corr[n + i]);
-                            tmem_st32(t_lane + 128 + n, o);
+                            for (int i = 0; i < kCols; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.corr[n + i]);
+                            st_cols<kCols>(t_lane + 128 + n, o);
                         }
                         tc_before();
                     }
@@ -428,10 +403,11 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             more = it.next(p, total);
             if (more) stage_q(it.b, it.h);
             // sums over the keys: halves of the nodes change lanes until a lane
-            // holds NP / 32 nodes' sums over its warp
+            // holds NP / 32 nodes' sums over its warp (or two lanes one node's)
 #pragma unroll
             for (int half = NP / 2, off = 16; off > 0; half >>= 1, off >>= 1) {
                 const bool up = lane & off;
+                if (half == 0) l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
 #pragma unroll
                 for (int n = 0; n < half; ++n) {
                     const float give = up ? l[n] : l[n + half], keep = up ? l[n + half] : l[n];
@@ -440,7 +416,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             }
             // lane bits, highest first, chose the halves: lane i holds nodes i * NP / 32 ...
 #pragma unroll
-            for (int n = 0; n < NP / 32; ++n) sh.part[warp][lane * (NP / 32) + n] = l[n];
+            for (int n = 0; n < (NP + 31) / 32; ++n) sh.part[warp][lane * NP / 32 + n] = l[n];
             if (!(ok = sync())) break;
             const size_t rowbase = ((size_t)b * p.slots_per_b + p.slot0[h] + slot) * p.N;
             ok = mbar_wait(&sh.copied[items & 3], (items >> 2) & 1, &sh.abort) && mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
@@ -454,11 +430,11 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             ++items;
             tc_after();
 #pragma unroll 1
-            for (int n = 0; n < NP; n += 32) {
-                uint32_t o[32];
-                tmem_ld32(t_lane + 128 + n, o);
+            for (int n = 0; n < NP; n += kCols) {
+                uint32_t o[kCols];
+                ld_cols<kCols>(t_lane + 128 + n, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < kCols; ++i)
                     if (n + i < p.N) p.part[(rowbase + n + i) * kD + tid] = __uint_as_float(o[i]);
             }
             tc_before();
@@ -500,7 +476,7 @@ bool tree_tc_pages(int page_rows) {
 }
 
 cudaError_t launch_tree_tc(const TreeParams &p, cudaStream_t s) {
-    return p.N <= 32 ? launch_np<32>(p, s) : launch_np<64>(p, s);
+    return p.N <= 16 ? launch_np<16>(p, s) : p.N <= 32 ? launch_np<32>(p, s) : launch_np<64>(p, s);
 }
 
 }  // namespace rat

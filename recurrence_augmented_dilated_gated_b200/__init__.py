@@ -384,8 +384,16 @@ def rat_decode_step_paged(cfg, q, k, v, g, state_k, state_v, cache, cache_cap, p
 # ------------------------------------------------------------- drafted trees
 
 
+# The raw handle of a device's current stream without building a Stream object
+# (3 us of a 20 us call); the public way where torch has no such function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Args:
     """Arguments of one call: checked tensors of one device, on which it runs."""
+
+    __slots__ = ("index", "ws", "ws_bytes")
 
     def __init__(self, ws):
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda:
@@ -396,7 +404,7 @@ class _Args:
 
     def ptr(self, t, name, dtype, shape, optional=False):
         # the usual case in a few attribute reads: a decode step is as short as these checks
-        if (isinstance(t, torch.Tensor) and t.dtype == dtype and (shape is None or t.shape == shape)
+        if (type(t) is torch.Tensor and t.dtype is dtype and (shape is None or t.shape == shape)
                 and t.get_device() == self.index and t.is_contiguous()):
             return t.data_ptr() or None
         p = _ptr(t, name, dtype, shape, optional)
@@ -404,15 +412,19 @@ class _Args:
             raise ValueError("%s is on %s, the workspace on cuda:%d" % (name, t.device, self.index))
         return p
 
-    def call(self, fn, what, *args, stream=None):
-        if isinstance(stream, torch.cuda.Stream) and stream.device.index != self.index:
-            raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, self.index))
+    def call(self, what, *args, stream=None):
+        if isinstance(stream, torch.cuda.Stream):
+            if stream.device.index != self.index:
+                raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, self.index))
+            stream = stream.cuda_stream
+        fn = getattr(load_library(), what)
         if torch.cuda.current_device() == self.index:
-            rc = fn(*args, self.ws, self.ws_bytes, _stream(stream))
+            rc = fn(*args, self.ws, self.ws_bytes, _raw_stream(self.index) if stream is None else int(stream))
         else:
             with torch.cuda.device(self.index):
-                rc = fn(*args, self.ws, self.ws_bytes, _stream(stream))
-        _check(rc, what)
+                rc = fn(*args, self.ws, self.ws_bytes, _raw_stream(self.index) if stream is None else int(stream))
+        if rc != RAT_OK:
+            _check(rc, what)
 
 
 def _paged_desc(a, cfg, cache):
@@ -424,21 +436,27 @@ def _paged_desc(a, cfg, cache):
     return ctypes.byref(cache)
 
 
-def _tree_step(what, cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse, ws, stream):
+def _tree_shapes(a, cfg, cache, cache_cap):
+    """(B, N, H, shape of token tensors, of states, element type, cache arguments) of a tree call."""
     c = cfg.c
-    tok, st, dt = (c.B, c.T, c.H, c.d), (c.B, c.H, c.d), cfg.torch_dtype
-    a = _Args(ws)
-    if isinstance(cache, tuple):
-        cshape = (c.B, c.H, rat_cache_rows(cfg, cache_cap), c.d)
-        where = [a.ptr(cache[0], "cache_k", dt, cshape), a.ptr(cache[1], "cache_v", dt, cshape)]
+    B, N, H, d, dt = c.B, c.T, c.H, c.d, cfg.torch_dtype
+    if type(cache) is tuple:
+        shape = (B, H, rat_cache_rows(cfg, cache_cap), d)
+        where = (a.ptr(cache[0], "cache_k", dt, shape), a.ptr(cache[1], "cache_v", dt, shape))
     else:
-        where = [_paged_desc(a, cfg, cache)]
-    a.call(getattr(load_library(), what), what, cfg.ref(), a.ptr(q, "q", dt, tok), a.ptr(k, "k", dt, tok),
+        where = (_paged_desc(a, cfg, cache),)
+    return B, N, H, (B, N, H, d), (B, H, d), dt, where
+
+
+def _tree_step(what, cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse, ws, stream):
+    a = _Args(ws)
+    B, N, H, tok, st, dt, where = _tree_shapes(a, cfg, cache, cache_cap)
+    a.call(what, cfg.ref(), a.ptr(q, "q", dt, tok), a.ptr(k, "k", dt, tok),
            a.ptr(v, "v", dt, tok), a.ptr(g, "g", dt, cfg.gate_shape(tok)),
-           a.ptr(parent, "parent", torch.int32, (c.B, c.T)), a.ptr(state_k, "state_k", torch.float32, st),
+           a.ptr(parent, "parent", torch.int32, (B, N)), a.ptr(state_k, "state_k", torch.float32, st),
            a.ptr(state_v, "state_v", torch.float32, st), *where, int(cache_cap),
-           a.ptr(pos, "pos", torch.int32, (c.B,)), a.ptr(o, "o", dt, tok),
-           a.ptr(lse, "lse", torch.float32, (c.B, c.H, c.T), True), stream=stream)
+           a.ptr(pos, "pos", torch.int32, (B,)), a.ptr(o, "o", dt, tok),
+           a.ptr(lse, "lse", torch.float32, (B, H, N), True), stream=stream)
 
 
 def rat_tree_decode_step(cfg, q, k, v, g, parent, state_k, state_v, cache_k, cache_v, cache_cap, pos, o, lse=None,
@@ -459,20 +477,14 @@ def rat_tree_decode_step_paged(cfg, q, k, v, g, parent, state_k, state_v, cache,
 
 def _tree_commit(what, cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache, cache_cap, pos,
                  out_pos, ws, stream):
-    c = cfg.c
-    tok, st, dt = (c.B, c.T, c.H, c.d), (c.B, c.H, c.d), cfg.torch_dtype
     f32, i32 = torch.float32, torch.int32
     a = _Args(ws)
-    if isinstance(cache, tuple):
-        cshape = (c.B, c.H, rat_cache_rows(cfg, cache_cap), c.d)
-        where = [a.ptr(cache[0], "cache_k", dt, cshape), a.ptr(cache[1], "cache_v", dt, cshape)]
-    else:
-        where = [_paged_desc(a, cfg, cache)]
-    a.call(getattr(load_library(), what), what, cfg.ref(), a.ptr(k, "k", dt, tok), a.ptr(v, "v", dt, tok),
-           a.ptr(g, "g", dt, cfg.gate_shape(tok)), a.ptr(parent, "parent", i32, (c.B, c.T)),
-           a.ptr(leaf, "leaf", i32, (c.B,)), a.ptr(state_k, "state_k", f32, st), a.ptr(state_v, "state_v", f32, st),
+    B, N, H, tok, st, dt, where = _tree_shapes(a, cfg, cache, cache_cap)
+    a.call(what, cfg.ref(), a.ptr(k, "k", dt, tok), a.ptr(v, "v", dt, tok),
+           a.ptr(g, "g", dt, cfg.gate_shape(tok)), a.ptr(parent, "parent", i32, (B, N)),
+           a.ptr(leaf, "leaf", i32, (B,)), a.ptr(state_k, "state_k", f32, st), a.ptr(state_v, "state_v", f32, st),
            a.ptr(out_state_k, "out_state_k", f32, st), a.ptr(out_state_v, "out_state_v", f32, st), *where,
-           int(cache_cap), a.ptr(pos, "pos", i32, (c.B,)), a.ptr(out_pos, "out_pos", i32, (c.B,)), stream=stream)
+           int(cache_cap), a.ptr(pos, "pos", i32, (B,)), a.ptr(out_pos, "out_pos", i32, (B,)), stream=stream)
 
 
 def rat_tree_commit(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache_k, cache_v,
@@ -499,7 +511,7 @@ def rat_page_table_update(cfg, page_table, page_rows, num_pages, cache_cap, leng
     i32 = torch.int32
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != c.B:
         raise ValueError("page_table must be [B, pages_per_seq]")
-    a.call(load_library().rat_page_table_update, "rat_page_table_update", cfg.ref(),
+    a.call("rat_page_table_update", cfg.ref(),
            a.ptr(page_table, "page_table", i32, None), int(page_rows), int(page_table.shape[1]), int(num_pages),
            int(cache_cap), a.ptr(length, "length", i32, (c.B,)), int(extra),
            a.ptr(free_pages, "free_pages", i32, (int(num_pages),)), a.ptr(n_free, "n_free", i32, (1,)), stream=stream)
@@ -511,7 +523,7 @@ def rat_slot_map(cfg, cache, cache_cap, pos, count, slots, ring_slots=None, ws=N
     c = cfg.c
     a = _Args(ws)
     shape = (c.B, c.T, c.H)
-    a.call(load_library().rat_slot_map, "rat_slot_map", cfg.ref(),
+    a.call("rat_slot_map", cfg.ref(),
            None if cache is None else _paged_desc(a, cfg, cache), int(cache_cap),
            a.ptr(pos, "pos", torch.int32, (c.B,)), a.ptr(count, "count", torch.int32, (c.B,), True),
            a.ptr(slots, "slots", torch.int64, shape), a.ptr(ring_slots, "ring_slots", torch.int64, shape, True),

@@ -649,8 +649,14 @@ size_t rat_workspace_size(const rat_cfg *cfg, int op, int cache_cap) {
         if (op == RAT_OP_STATUS) return sizeof(WsHeader);
         TreeParams p;
         TreeLayout tl;
-        if (plan_tree(&tmp, cache_cap, 0, &p, &tl) != RAT_OK) return 0;
-        return sizeof(WsHeader) + tl.total;
+        // one size for every cache: pages that do not suit the tcgen05 form (one row)
+        // change how the rows are cut
+        size_t need = 0;
+        for (int page_rows = 0; page_rows < 2; ++page_rows) {
+            if (plan_tree(&tmp, cache_cap, page_rows, &p, &tl) != RAT_OK) return 0;
+            need = std::max(need, tl.total);
+        }
+        return sizeof(WsHeader) + need;
     }
     if (check_cfg(cfg, !dec) != RAT_OK) return 0;
     if (dec && cache_cap < 1) return 0;

@@ -9,6 +9,20 @@ namespace rat {
 // Nodes of one entry's tree, at most: a branch fits in one 64-bit mask.
 constexpr int kTreeMaxNodes = 64;
 
+// What the plan says of one head: in one place, as the first read of a kernel
+// parameter's line by an SM takes as long as one of global memory.
+struct TreeHead {
+    int dil, win;
+    int slab;        // ceil(cap / dil)
+    int nsplit;      // pieces of one dilated set, at most
+    int wsplit;      // pieces of the window's held rows (>= 1)
+    int slab_ctas;   // CTAs that share the head's (set, piece) items
+    int cta0;        // first CTA of the head within an entry
+    int slot0;       // first partial slot
+    int recur;
+    int fused;       // one item has all the keys and writes the result itself
+};
+
 struct TreeParams {
     const void *q, *k, *v, *g;   // [B,N,H,d]
     const int *parent;           // device [B,N]
@@ -20,7 +34,7 @@ struct TreeParams {
     void *node_rows;             // [B][H][2][N][d] augmented rows of the nodes (cfg dtype)
     float *part;                 // [B][slots_per_b][N][d] unnormalised accumulators
     float2 *ml;                  // [B][slots_per_b][N] (max, sum); sum < 0: a page was not valid
-    int *info;                   // [B][H][N] pieces of the node's dilated set; -1: absent, or entry skipped
+    int *info;                   // [B][H][N] pieces of the node's dilated set; -1: absent, or entry skipped; -2: done
     long long cache_R;
     int cap, B, N, H, d;
     int grid, dedupe, sep;       // as in DecodeParams
@@ -29,15 +43,7 @@ struct TreeParams {
     float scale_log2;
     int ctas_per_b, slots_per_b;
     int ctas_per_head;           // when all heads have as many, else 0
-    int dil[kMaxHeads];
-    int win[kMaxHeads];
-    int slab[kMaxHeads];         // ceil(cap / dil)
-    int nsplit[kMaxHeads];       // pieces of one dilated set, at most
-    int wsplit[kMaxHeads];       // pieces of the window's held rows (>= 1)
-    int slab_ctas[kMaxHeads];    // CTAs that share the head's (set, piece) items
-    int cta0[kMaxHeads + 1];     // first CTA of head h within an entry
-    int slot0[kMaxHeads + 1];    // first partial slot of head h within an entry
-    unsigned char recur[kMaxHeads];
+    TreeHead head[kMaxHeads];
     // heads whose held rows tree_tc.cu takes (slab_ctas is 0), and their pieces
     int n_tc, tc_items_per_b;
     unsigned char tc_head[kMaxHeads];
@@ -48,6 +54,7 @@ struct TreeParams {
 // The shape of one entry's tree, in shared memory.
 struct TreeInfo {
     unsigned long long anc[kTreeMaxNodes];  // branch of node i, itself included (0: absent)
+    unsigned long long far;                 // tree_masks()
     int jump[kTreeMaxNodes];
     signed char depth[kTreeMaxNodes];       // -1: absent
     int max_depth;                          // -1: no node
@@ -133,13 +140,13 @@ __device__ __forceinline__ int tree_set_of(const TreeParams &p, int D, int depth
 }
 // Held rows of set g, and the first cache row of its slab.
 __device__ __forceinline__ int tree_set_rows(const TreeParams &p, int h, int pos, int g, long long &row0) {
-    const int D = p.dil[h];
+    const int D = p.head[h].dil;
     if (p.grid) {
         row0 = 0;
         return pos / D;
     }
     const int r = (int)(((unsigned)pos + g) % (unsigned)D);
-    row0 = (long long)r * p.slab[h];
+    row0 = (long long)r * p.head[h].slab;
     return pos > r ? (pos - 1 - r) / D + 1 : 0;
 }
 // How n rows are cut: at most `most` pieces of equal length, in whole 128 rows
@@ -154,8 +161,15 @@ __device__ __forceinline__ int tree_piece_rows(int n, int most) {
 // decode step (logits beyond +-80 saturate).
 __device__ __forceinline__ void gate_pair(float g, float &a, float &oma) {
     const float e = expf(-fminf(fmaxf(g, -80.f), 80.f));
-    a = 1.f / (1.f + e);
+    a = __fdividef(1.f, 1.f + e);   // within 2 units of the last place; 1 + e < 2^126
     oma = e * a;
+}
+
+__device__ __forceinline__ void gate4(const float4 &g, float4 &a, float4 &oma) {
+    gate_pair(g.x, a.x, oma.x);
+    gate_pair(g.y, a.y, oma.y);
+    gate_pair(g.z, a.z, oma.z);
+    gate_pair(g.w, a.w, oma.w);
 }
 
 // Split plan and workspace offsets of a tree step (host); returns the bytes the
@@ -166,8 +180,8 @@ struct TreeLayout {
 TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p);
 
 cudaError_t launch_tree(const TreeParams &p, int dtype, cudaStream_t s);
-// the attention part of a bf16 step (tree_mma.cu)
-cudaError_t launch_tree_mma(const TreeParams &p, unsigned grid, cudaStream_t s);
+// recurrence, windows, nodes and the slabs of all heads but those in tc_head (tree_mma.cu)
+cudaError_t launch_tree_mma(const TreeParams &p, int dtype, unsigned grid, cudaStream_t s);
 // the held rows of its heads in tc_head (tree_tc.cu), and whether pages of
 // page_rows rows suit its copies (0: a dense cache)
 bool tree_tc_pages(int page_rows);

@@ -33,13 +33,6 @@ __device__ __forceinline__ void step4(float4 &s, const float4 &x, const float4 &
     s.z = a.z * s.z + oma.z * x.z;
     s.w = a.w * s.w + oma.w * x.w;
 }
-__device__ __forceinline__ void gate4(const float4 &g, float4 &a, float4 &oma) {
-    gate_pair(g.x, a.x, oma.x);
-    gate_pair(g.y, a.y, oma.y);
-    gate_pair(g.z, a.z, oma.z);
-    gate_pair(g.w, a.w, oma.w);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParams p) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();

@@ -13,7 +13,7 @@ __device__ __forceinline__ int find_tree_head(const TreeParams &p, int it) {
     int lo = 0, hi = p.H - 1;  // largest h with cta0[h] <= it
     while (lo < hi) {
         int mid = (lo + hi + 1) >> 1;
-        if (p.cta0[mid] <= it) lo = mid; else hi = mid - 1;
+        if (p.head[mid].cta0 <= it) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
@@ -34,9 +34,9 @@ __device__ __forceinline__ long long key_offset(const TreeParams &p, const Keys 
     if (ks.kind == kNodes) return (bh * 2 * p.N + i) * p.d;   // keys; values N * d further
     unsigned row = (unsigned)ks.row0 + i;
     if (ks.kind == kWindow) {
-        const unsigned j = row, D = p.dil[h], S = p.slab[h];
+        const unsigned j = row, D = p.head[h].dil, S = p.head[h].slab;
         if (!p.grid) row = D == 1 ? j : j % D * S + j / D;
-        else row = D > 1 ? S + j % (unsigned)p.win[h] : j;   // the ring
+        else row = D > 1 ? S + j % (unsigned)p.head[h].win : j;   // the ring
     }
     if (!p.page_table) return (bh * p.cache_R + row) * p.d;
     const unsigned pi = row / (unsigned)p.page_rows, pr = row - pi * p.page_rows;
@@ -45,12 +45,26 @@ __device__ __forceinline__ long long key_offset(const TreeParams &p, const Keys 
     return (((long long)pg * p.H + h) * p.page_rows + pr) * p.d;
 }
 
+// Depth differences that are multiples of a head's dilation, and the nodes on its
+// grid, as bits (one warp).
+__device__ __forceinline__ void tree_masks(const TreeParams &p, TreeInfo &ti, int h, int pos) {
+    const int lane = threadIdx.x & 31;
+    const unsigned D = p.head[h].dil;
+    unsigned m[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        m[u] = __ballot_sync(0xffffffffu, p.grid ? ti.depth[i] >= 0 && (unsigned)(pos + ti.depth[i]) % D == D - 1 : i % D == 0);
+    }
+    if (lane == 0) ti.far = (unsigned long long)m[1] << 32 | m[0];
+}
+
 // How often key i counts for a node of depth `dep` and branch `anc` (0, 1 or 2).
 __device__ __forceinline__ int key_count(const TreeParams &p, const Keys &ks, const TreeInfo &ti, int h, int pos,
                                          int dep, unsigned long long anc, int node, int i) {
     if (i >= ks.n) return 0;
     if (ks.kind == kSlab) return 1;
-    const int D = p.dil[h], W = p.win[h];
+    const int D = p.head[h].dil, W = p.head[h].win;
     if (ks.kind == kWindow) {
         const int j = (int)ks.row0 + i, t = pos + dep;
         if (j <= t - W) return 0;
@@ -59,7 +73,7 @@ __device__ __forceinline__ int key_count(const TreeParams &p, const Keys &ks, co
     }
     if (!((anc >> i) & 1ull)) return 0;
     const int back = dep - ti.depth[i];
-    const int far = p.grid ? (i == node || (pos + ti.depth[i]) % D == D - 1) : back % D == 0;
+    const int far = p.grid ? i == node || ((ti.far >> i) & 1ull) : (int)((ti.far >> back) & 1ull);
     const int near = back < W && !(p.dedupe && far);
     return far + near;
 }
@@ -67,30 +81,37 @@ __device__ __forceinline__ int key_count(const TreeParams &p, const Keys &ks, co
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// The keys of a head's local item `li`: a piece of the window's held rows, and
-// in item 0 the nodes.  Returns the number of parts.
-__device__ __forceinline__ int local_keys(const TreeParams &p, int h, int pos, int li, Keys *parts) {
-    const int ws = p.wsplit[h], W = p.win[h];
-    const int n_held = W > 0 ? min(W - 1, pos) : 0, len = (n_held + ws - 1) / ws;
-    const int a = min(li * len, n_held);
-    parts[0].kind = kWindow;
-    parts[0].row0 = pos - n_held + a;
-    parts[0].n = min(len, n_held - a);
-    parts[1].kind = kNodes;
-    parts[1].row0 = 0;
-    parts[1].n = p.N;
-    return li == 0 ? 2 : 1;
-}
-
 // The rows of piece `piece` of set g; false when there is none.
 __device__ __forceinline__ bool slab_keys(const TreeParams &p, int h, int pos, int g, int piece, Keys &ks) {
     ks.kind = kSlab;
     const int n = tree_set_rows(p, h, pos, g, ks.row0);
-    const int len = tree_piece_rows(n, p.nsplit[h]);
+    const int len = tree_piece_rows(n, p.head[h].nsplit);
     if (n == 0 || (long long)piece * len >= n) return false;
     ks.row0 += piece * len;
     ks.n = min(len, n - piece * len);
     return true;
+}
+
+// The keys of a head's local item `li`: a piece of the window's held rows, in
+// item 0 the nodes, and the held rows of the dilated set if the head's keys are
+// all in one item.  Returns the number of parts.
+__device__ __forceinline__ int local_keys(const TreeParams &p, int h, int pos, int li, Keys *parts) {
+    const int ws = p.head[h].wsplit, W = p.head[h].win;
+    const int n_held = W > 0 ? min(W - 1, pos) : 0, len = (n_held + ws - 1) / ws;
+    const int a = min(li * len, n_held);
+    int k = 0;
+    if (p.head[h].fused && slab_keys(p, h, pos, 0, 0, parts[0])) k = 1;
+    parts[k].kind = kWindow;
+    parts[k].row0 = pos - n_held + a;
+    parts[k].n = min(len, n_held - a);
+    if (parts[k].n > 0) ++k;
+    if (li == 0) {
+        parts[k].kind = kNodes;
+        parts[k].row0 = 0;
+        parts[k].n = p.N;
+        ++k;
+    }
+    return k;
 }
 
 // What tree_combine_kernel needs to know of the tree (item 0 of every head).
@@ -100,10 +121,11 @@ __device__ __forceinline__ void tell_pieces(const TreeParams &p, const TreeInfo 
     int np = -1;
     if (ti.valid && ti.depth[i] >= 0) {
         long long row0;
-        const int n = tree_set_rows(p, h, pos, tree_set_of(p, p.dil[h], ti.depth[i]), row0);
-        const int len = tree_piece_rows(n, p.nsplit[h]);
+        const int n = tree_set_rows(p, h, pos, tree_set_of(p, p.head[h].dil, ti.depth[i]), row0);
+        const int len = tree_piece_rows(n, p.head[h].nsplit);
         np = n == 0 ? 0 : (n + len - 1) / len;
     }
+    if (ti.valid && p.head[h].fused) np = -2;   // absent nodes too
     p.info[((size_t)b * p.H + h) * p.N + i] = np;
 }
 
@@ -133,7 +155,7 @@ __device__ __forceinline__ void list_nodes(const TreeParams &p, const TreeInfo &
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int i = lane + 32 * u;
-        const bool in = ti.depth[i] >= 0 && tree_set_of(p, p.dil[h], ti.depth[i]) == g;
+        const bool in = ti.depth[i] >= 0 && tree_set_of(p, p.head[h].dil, ti.depth[i]) == g;
         const unsigned mask = __ballot_sync(0xffffffffu, in);
         if (in) nodes[cnt + __popc(mask & ((1u << lane) - 1u))] = i;
         cnt += __popc(mask);
@@ -148,66 +170,102 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool o
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The recurrence down the tree (128 threads).  A thread owns one channel of both
-// tensors (D = 128) or of one (D = 64: the upper half of the CTA takes the
-// values) and walks the nodes in order, a parent before its children.  k, v and
-// g of as many nodes as fit in kTreeStage bytes are staged together by
-// asynchronous copies: one round trip to memory for 32 nodes of bf16, not one
-// per node.  Shared memory: the states, a column per thread ([node][2 D] floats),
-// then the stage.  The code is kept small (no unrolled chunk): it runs once per
-// CTA, and fetching a straight line of instructions cold costs more than the
-// loop (measured: 40 us a CTA with 16 nodes unrolled).
-constexpr int kTreeStage = 32768;
-template <int D> constexpr size_t tree_smem(int N) { return (size_t)N * 2 * D * sizeof(float) + kTreeStage; }
+// The recurrence down the tree (128 threads), 64 channels at a time, in shared
+// memory as [node][array][64] floats: arrays k, v, gate and, with separate gates,
+// the values' gate.
+//   1  the tokens of all nodes are copied into their places (one round trip);
+//   2  half a warp a node, each place is overwritten: k and v by (1 - a) x, a gate
+//      by a;
+//   3  a thread, one channel of one tensor, walks the nodes, a parent before its
+//      children, adding a * parent: the rest is out of the chain;
+//   4  the rows are rounded and written out together.
+// (Gates inside the walk took 500 cycles a node, 23 us for 64 nodes.)  The code is
+// kept small: it runs once per CTA, and a straight line of instructions fetched
+// cold costs more than a loop.  The memory stays within a bf16 ring's 64 KB, so
+// that three CTAs share an SM (two took the hybrid step from 377 to 412 us).
+constexpr int kTreeChannels = 64;
+constexpr size_t tree_smem(int N, int sep) { return (size_t)N * kTreeChannels * (sep ? 4 : 3) * sizeof(float); }
 
 template <typename T, int D>
-__device__ __forceinline__ void run_tree(const TreeParams &p, const int *parent, int b, int h, uint8_t *smem) {
-    constexpr int kThreads = 128, kBoth = D == kThreads ? 2 : 1;
-    constexpr int kChunks = D * (int)sizeof(T) / 16;                 // 16-byte chunks of a row
-    constexpr int kNodes = kTreeStage / (4 * D * (int)sizeof(T));    // nodes staged at a time (k, v, two gates)
-    static_assert(D * 2 == kThreads * kBoth, "the CTA's threads cover the channels of both tensors");
-    const int tid = threadIdx.x, c = tid % D, x0 = tid / D;
+__device__ __forceinline__ void run_tree(const TreeParams &p, const int *parent, int b, int h, float *mem) {
+    constexpr int kThreads = 128, kCh = kTreeChannels;
+    constexpr int kChunks = kCh * (int)sizeof(T) / 16;               // 16-byte chunks of 64 channels
+    const int tid = threadIdx.x, N = p.N;
+    const int arrays = p.sep ? 4 : 3, row = arrays * kCh;            // floats of a node
     const size_t bh = (size_t)b * p.H + h;
-    const bool rec = p.recur[h] != 0;
-    const int n_src = !rec ? 2 : p.sep ? 4 : 3;
-    float *hc = reinterpret_cast<float *>(smem) + tid;   // [node][kBoth][thread]: no other thread reads this column
-    uint8_t *stage = smem + (size_t)p.N * 2 * D * sizeof(float);
-    const float s0 = p.state[x0][bh * D + c], s1 = kBoth == 2 ? p.state[1][bh * D + c] : 0.f;
-    T *out = static_cast<T *>(p.node_rows) + (bh * 2 + x0) * p.N * D + c;
-    for (int n0 = 0; n0 < p.N; n0 += kNodes) {
-        const int nn = min(kNodes, p.N - n0);
-        __syncthreads();   // the stage is free
+    const bool rec = p.head[h].recur != 0;
+    const int c = tid % kCh, x = tid / kCh;
 #pragma unroll 1
-        for (int y = 0; y < n_src; ++y) {
-            const char *src = static_cast<const char *>(y == 0 ? p.k : y == 1 ? p.v : p.g) +
-                              (y == 3 ? (size_t)p.B * p.N * p.H * D * sizeof(T) : 0);
+    for (int c0 = 0; c0 < D; c0 += kCh) {
+        const float s0 = p.state[x][bh * D + c0 + c];
+        __syncthreads();   // the channels before are written out
 #pragma unroll 1
-            for (int e = tid; e < nn * kChunks; e += kThreads) {
+        for (int y = 0; y < (rec ? arrays : 2); ++y) {
+            const T *src = static_cast<const T *>(y == 0 ? p.k : y == 1 ? p.v : p.g) + (y == 3 ? (size_t)p.B * N * p.H * D : 0) + c0;
+#pragma unroll 2
+            for (int e = tid; e < N * kChunks; e += kThreads) {
                 const int n = e / kChunks, ch = e % kChunks;
-                cp_async16(smem_u32(stage) + ((y * kNodes + n) * kChunks + ch) * 16,
-                           src + ((((size_t)b * p.N + n0 + n) * p.H + h) * kChunks + ch) * 16, true);
+                cp_async16(smem_u32(mem + n * row + y * kCh) + ch * 16,
+                           src + (((size_t)b * N + n) * p.H + h) * D + ch * (16 / (int)sizeof(T)), true);
             }
         }
         cp_commit();
         cp_wait<0>();
         __syncthreads();
-        const T *st = reinterpret_cast<const T *>(stage) + c;
-#pragma unroll 2
-        for (int w = 0; w < nn; ++w) {
-            const int n = n0 + w, par = parent[n];
-            float a = 0.f, oma = 1.f;
-            if (rec) gate_pair((float)st[((p.sep && x0 ? 3 : 2) * kNodes + w) * D], a, oma);
-            float s = a * (par >= 0 ? hc[(size_t)par * kBoth * kThreads] : s0) + oma * (float)st[(x0 * kNodes + w) * D];
-            if (par == RAT_NODE_ABSENT) s = 0.f;   // its inputs may hold anything
-            hc[(size_t)n * kBoth * kThreads] = s;
-            store1(out + (size_t)n * D, s);
-            if (kBoth == 2) {
-                if (rec && p.sep) gate_pair((float)st[(3 * kNodes + w) * D], a, oma);
-                s = a * (par >= 0 ? hc[(size_t)(par * 2 + 1) * kThreads] : s1) + oma * (float)st[(kNodes + w) * D];
-                if (par == RAT_NODE_ABSENT) s = 0.f;
-                hc[(size_t)(n * 2 + 1) * kThreads] = s;
-                store1(out + (size_t)(p.N + n) * D, s);
+#pragma unroll 1
+        for (int n0 = 0; n0 < N; n0 += kThreads / 16) {
+            const int n = n0 + tid / 16;
+            float *m = mem + n * row + (tid % 16) * 4;
+            const T *raw = reinterpret_cast<const T *>(mem + n * row) + (tid % 16) * 4;
+            constexpr int kStep = kCh * (int)(sizeof(float) / sizeof(T));   // from array to array
+            float4 k, v, g, gv;
+            if (n < N) {
+                k = IO4<T>::load(raw);
+                v = IO4<T>::load(raw + kStep);
+                if (rec) g = IO4<T>::load(raw + 2 * kStep);
+                if (rec && p.sep) gv = IO4<T>::load(raw + 3 * kStep);
             }
+            __syncwarp();
+            if (n < N) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), oma = make_float4(1.f, 1.f, 1.f, 1.f);
+                if (rec) gate4(g, a, oma);
+                *reinterpret_cast<float4 *>(m) = make_float4(oma.x * k.x, oma.y * k.y, oma.z * k.z, oma.w * k.w);
+                *reinterpret_cast<float4 *>(m + 2 * kCh) = a;
+                if (p.sep) {
+                    if (rec) gate4(gv, a, oma);
+                    *reinterpret_cast<float4 *>(m + 3 * kCh) = a;
+                }
+                *reinterpret_cast<float4 *>(m + kCh) = make_float4(oma.x * v.x, oma.y * v.y, oma.z * v.z, oma.w * v.w);
+            }
+        }
+        __syncthreads();
+        float *m = mem + x * kCh + c;
+        const float *ga = mem + (2 + (p.sep ? x : 0)) * kCh + c;
+#pragma unroll 1
+        for (int n0 = 0; n0 < N; n0 += 4) {
+            float a[4], u[4];
+            int par[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int n = min(n0 + w, N - 1);
+                par[w] = parent[n];
+                u[w] = m[n * row];
+                a[w] = ga[n * row];
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (n0 + w < N) {
+                    const float s = a[w] * (par[w] >= 0 ? m[par[w] * row] : s0) + u[w];
+                    m[(n0 + w) * row] = par[w] == RAT_NODE_ABSENT ? 0.f : s;   // its inputs may hold anything
+                }
+            }
+        }
+        __syncthreads();
+        T *out = static_cast<T *>(p.node_rows) + bh * 2 * N * D + c0;
+#pragma unroll 2
+        for (int e = tid; e < N * 2 * (kCh / 4); e += kThreads) {
+            const int ch = e % (kCh / 4), nx = e / (kCh / 4), y = nx & 1, n = nx >> 1;
+            IO4<T>::store(out + ((size_t)y * N + n) * D + ch * 4, *reinterpret_cast<const float4 *>(mem + n * row + y * kCh + ch * 4));
         }
     }
     __threadfence();   // other threads copy these rows past L1

@@ -1,23 +1,29 @@
-// tree_mma.cu -- K7 with bf16 operands: the tree step's items (tree.cu) on the
-// tensor cores.
+// tree_mma.cu -- K7: the tree step's items (tree.cu) on the register-fragment
+// tensor-core instructions, bf16 and fp32.
 //
 // An item is a run of cache rows and the nodes that read it: scores S = Q K~^T,
 // probabilities P, sums O = P V~, with 16 nodes as the rows of one matrix
-// instruction (m16n8k16, fp32 accumulation).  A node's rows of S and O stay in
-// registers for the whole item; K~ and V~ rows pass through a ring of shared
-// memory filled by 16-byte asynchronous copies, in tiles of kTile rows.
-//   - up to 16 nodes: the four warps take different keys of the tile and join
+// instruction.  A node's rows of S and O stay in registers for the whole item;
+// K~ and V~ rows pass through a ring of shared memory, by TMA from a dense
+// cache, by 16-byte asynchronous copies row by row from pages, the window and
+// the tree.
+//   - up to 16 nodes: the four warps take different keys of a tile and join
 //     their partial softmaxes at the end; up to 32: two by two; up to 64: a
 //     warp for every 16 nodes.  So every warp works whatever the tree's shape.
-//   - 16-byte chunk c of row r sits at chunk c ^ (r & 7): the eight rows of an
-//     ldmatrix fall on different banks.
+//   - 16-byte chunk c of row r sits at chunk c ^ (r & 7) of its 128 bytes: the
+//     eight rows of an ldmatrix fall on different banks.
 //   - the softmax reference of a node is raised only when a score passes it by
-//     more than 2^8 (P stays below 2^8, its sum in fp32): one vote per 16 keys
-//     instead of reductions and rescaling.
-//   - P is rounded to bf16 for the product with V~ (half a step, 2^-9 of each
-//     probability; the sum of P keeps fp32): the same rounding as the prefill's.
-// Bound: HBM for small node counts (a row's 4 d bytes are used for 4 d
-// operations per node).
+//     more than 2^8 (P stays below 2^8, its sum in fp32): one vote per block of
+//     keys instead of reductions and rescaling.
+//   - bf16: m16n8k16.  P is rounded to bf16 for the product with V~ (half a
+//     step, 2^-9 of each probability; the sum of P keeps fp32): the same
+//     rounding as the prefill's.
+//   - fp32: m16n8k8 on tf32 halves: x = b + s with b = x rounded to tf32 (11
+//     bits) and s = x - b, of which the instruction takes 11 bits too; x y = b b' +
+//     b s' + s b' leaves out s s' and what s was cut by, 2^-22 of the product.
+// Bound: HBM for small node counts (a row's bytes serve 4 d operations a node);
+// with more than 16 nodes on the same rows the instruction rate, which is why
+// tree_tc.cu takes those where it can.
 #include "attn_tc.cuh"
 #include "tree_keys.cuh"
 
@@ -27,8 +33,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 64;
-constexpr int kStages = 3;
+constexpr int kTileMax = 64;
+constexpr int kStagesMax = 2;
 constexpr float kSlack = 8.f;   // log2 of how far P may pass 1
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -44,22 +50,44 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = big + small, big with the 11 bits of tf32 (the instruction cuts small to as many)
+__device__ __forceinline__ void split(uint32_t x, uint32_t &big, uint32_t &small) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(big) : "f"(__uint_as_float(x)));
+    small = __float_as_uint(__uint_as_float(x) - __uint_as_float(big));
+}
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<uint32_t *>(&t);
 }
-__device__ __forceinline__ bool not_finite2(uint32_t w) {   // either bf16 of a pair
+template <typename T> __device__ __forceinline__ bool not_finite(uint32_t w) {   // any value in a word
+    if (sizeof(T) == 4) return (w & 0x7f800000u) == 0x7f800000u;
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-template <int D> struct Shape {
-    static constexpr int kChunks = D / 8;                   // 16-byte chunks of a row
-    static constexpr uint32_t kRowBytes = D * 2;
-    static constexpr uint32_t kHalf = kTile * kRowBytes;    // K~ of a stage, then V~
+template <typename T, int D> struct Shape {
+    static constexpr bool kF32 = sizeof(T) == 4;
+    static constexpr int kTile = kF32 && D == 128 ? 32 : 64;   // rows of a stage
+    static constexpr int kBlocks = kF32 ? kTile / 8 : 4;    // of kBlock keys
+    static constexpr int kBlock = kTile / kBlocks;          // keys that a warp takes at a time
+    static constexpr int kStages = 2;
+    static constexpr int kPer = 16 / (int)sizeof(T);        // channels of a 16-byte chunk
+    static constexpr int kChunks = D / kPer;                // chunks of a row
+    static constexpr uint32_t kHalf = kTile * D * sizeof(T);   // K~ of a stage, then V~
     static constexpr uint32_t kStage = 2 * kHalf;
+    static constexpr uint32_t kRing = kStages * kStage;
     static constexpr int kRowsAtOnce = kThreads / kChunks;  // rows that one pass of the CTA copies
-    // 16-byte chunk c of row r: halves of 64 channels, 128-byte swizzled as TMA writes them
-    static __device__ __forceinline__ uint32_t at(int r, int c) { return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+    static constexpr int kWarpRows = kTile / kWarps;        // rows that a warp copies of a tile
+    // 16-byte chunk c of row r of `rows`: 128-byte columns, swizzled as TMA writes them
+    static __device__ __forceinline__ uint32_t at(int r, int c, int rows = kTile) {
+        return (c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    }
 };
 
 // TMA maps of a dense cache; a paged one is copied row by row.
@@ -67,14 +95,18 @@ struct Maps {
     CUtensorMap kv[2];
 };
 
+// Rows of Q that the warps read: 16 for one, two or four of them.
+__host__ __device__ __forceinline__ int padded_nodes(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : 64; }
+
 struct Shared {
     TreeInfo ti;
     int parent[kTreeMaxNodes], nodes[kTreeMaxNodes];
     int n, bad, odd;                      // odd: some local value is not finite
-    uint64_t full[kStages];               // a slab's tile has landed
+    uint64_t full[kStagesMax];              // a slab's tile has landed
     volatile int abort;
-    uint8_t count[kTreeMaxNodes][kTile];  // how often a key of a masked tile counts for a node
+    uint8_t count[kTreeMaxNodes][kTileMax];  // how often a key of a masked tile counts for a node
     float m[kWarps][16], l[kWarps][16];
+    float inv[kTreeMaxNodes];
 };
 
 // One item: the keys of parts[0 .. n_parts), tile by tile, for the sh.n nodes of
@@ -82,35 +114,45 @@ struct Shared {
 // is and which tiles carry a mask): a second copy of it would only thrash the
 // instruction cache.
 // False when a wait gave up.
-template <int D>
+template <typename T, int D>
 __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, Shared &sh, uint8_t *ring, const Keys *parts,
                                          int n_parts, int b, int h, int pos, int slot, int &fills) {
-    using S = Shape<D>;
+    using S = Shape<T, D>;
+    constexpr int kTile = S::kTile, kStages = S::kStages, kBlock = S::kBlock, NB = kBlock / 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     fence_async();     // what was written to the ring by ordinary stores, before TMA writes there
     __syncthreads();   // sh.n and sh.nodes are set, and the ring is free
     const int n_nodes = sh.n;
-    const int WM = n_nodes <= 16 ? 1 : n_nodes <= 32 ? 2 : 4, WK = kWarps / WM;
+    const int WM = padded_nodes(n_nodes) / 16, WK = kWarps / WM;
     const int wm = warp % WM, wk = warp / WM;
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;   // this lane's row (and r0 + 8) and first column of a fragment
-    const int tiles0 = (parts[0].n + kTile - 1) / kTile;
-    const int n_tiles = tiles0 + (n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0);
+    // tiles of the parts, one part after the other
+    const int end0 = n_parts > 0 ? (parts[0].n + kTile - 1) / kTile : 0;
+    const int end1 = end0 + (n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0);
+    const int n_tiles = end1 + (n_parts > 2 ? (parts[2].n + kTile - 1) / kTile : 0);
+    auto part_of = [&](int t, int &k0) -> const Keys & {
+        const int i = (t >= end0) + (t >= end1);
+        k0 = (t - (i == 0 ? 0 : i == 1 ? end0 : end1)) * kTile;
+        return parts[i];
+    };
     if (tid == 0) sh.bad = sh.odd = 0;
-    const bool bulk = parts[0].kind == kSlab && !p.page_table;   // the item's tiles come by TMA
-    const int fill0 = fills;                                     // such tiles before this item's
-    if (bulk) fills += n_tiles;
+    const int bulk = n_parts > 0 && parts[0].kind == kSlab && !p.page_table ? end0 : 0;   // tiles that come by TMA
+    const int fill0 = fills;                                                              // such tiles before this item's
+    fills += bulk;
 
-    // Q into the stage that no tile uses yet
-    const uint32_t sq = smem_u32(ring) + ((fill0 + kStages - 1) % kStages) * S::kStage;
+    // Q: into the stage that no tile uses yet (bf16: it goes on to registers), or
+    // a place of its own (fp32: in halves it would be 128 registers)
+    const uint32_t sq = smem_u32(ring) + (S::kF32 ? S::kRing : ((fill0 + kStages - 1) % kStages) * S::kStage);
+    const int q_rows = S::kF32 ? padded_nodes(p.N) : kTreeMaxNodes;   // >= 16 WM
     for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
         const int r = e / S::kChunks, c = e % S::kChunks;
         const bool on = r < n_nodes;
         const int n = on ? sh.nodes[r] : 0;
-        cp_async16(sq + S::at(r, c), static_cast<const __nv_bfloat16 *>(p.q) + (((size_t)b * p.N + n) * p.H + h) * D + c * 8, on);
+        cp_async16(sq + S::at(r, c, q_rows), static_cast<const T *>(p.q) + (((size_t)b * p.N + n) * p.H + h) * D + c * S::kPer, on);
     }
     cp_commit();
     auto load = [&](int t) {
-        if (bulk) {
+        if (t < bulk) {
             if (tid == 0) {
                 const int f = fill0 + t, y = (int)parts[0].row0 + t * kTile;
                 uint64_t *bar = &sh.full[f % kStages];
@@ -119,22 +161,21 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int half = 0; half < D / 64; ++half)
-                        tma_load(dst + x * S::kHalf + half * (kTile * 128), &maps.kv[x], bar, half * 64, y, b * p.H + h);
+                    for (int col = 0; col < S::kChunks / 8; ++col)
+                        tma_load(dst + x * S::kHalf + col * (kTile * 128), &maps.kv[x], bar, col * 8 * S::kPer, y, b * p.H + h);
             }
             return;
         }
-        const bool second = t >= tiles0;
-        const Keys &ks = parts[second ? 1 : 0];
-        const int k0 = (second ? t - tiles0 : t) * kTile;
-        const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(p.cache[0]), *vb = static_cast<const __nv_bfloat16 *>(p.cache[1]);
+        int k0;
+        const Keys &ks = part_of(t, k0);
+        const T *kb = static_cast<const T *>(p.cache[0]), *vb = static_cast<const T *>(p.cache[1]);
         if (ks.kind == kNodes) {
-            kb = static_cast<const __nv_bfloat16 *>(p.node_rows);
+            kb = static_cast<const T *>(p.node_rows);
             vb = kb + (size_t)p.N * D;
         }
-        // a warp copies 16 rows; lane i finds the place of the i-th of them
+        // a warp copies kWarpRows rows; lane i finds the place of the i-th of them
         constexpr int kPerPass = 32 / S::kChunks;   // rows of a warp in one pass
-        const int mine = (lane & 15) / kPerPass * S::kRowsAtOnce + warp * kPerPass + (lane & 15) % kPerPass;
+        const int li = lane % S::kWarpRows, mine = li / kPerPass * S::kRowsAtOnce + warp * kPerPass + li % kPerPass;
         long long off = -1;
         if (k0 + mine < ks.n) {
             off = key_offset(p, ks, b, h, k0 + mine);
@@ -143,10 +184,10 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
         const uint32_t dst = smem_u32(ring) + ((fill0 + t) % kStages) * S::kStage;
         const int c = lane % S::kChunks;
 #pragma unroll
-        for (int i = 0; i < 16 / kPerPass; ++i) {
+        for (int i = 0; i < S::kWarpRows / kPerPass; ++i) {
             const long long o = __shfl_sync(0xffffffffu, off, i * kPerPass + lane / S::kChunks);
             const int r = i * S::kRowsAtOnce + warp * kPerPass + lane / S::kChunks;
-            const long long e = o < 0 ? 0 : o + c * 8;
+            const long long e = o < 0 ? 0 : o + c * S::kPer;
             cp_async16(dst + S::at(r, c), kb + e, o >= 0);
             cp_async16(dst + S::kHalf + S::at(r, c), vb + e, o >= 0);
         }
@@ -159,9 +200,26 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
     }
     cp_wait<kStages - 1>();
     __syncthreads();
-    uint32_t q[D / 16][4];   // the warp's nodes: rows of Q as A fragments
+    const uint32_t sq_small = sq + q_rows * D * 4;   // fp32: Q in halves, the small ones behind the big
+    if constexpr (S::kF32) {
+        uint4 *x = reinterpret_cast<uint4 *>(ring + S::kRing);
+        for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
+            uint4 *big = x + S::at(e / S::kChunks, e % S::kChunks, q_rows) / 16, *small = big + q_rows * D / 4;
+            const uint4 v = *big;
+            split(v.x, big->x, small->x);
+            split(v.y, big->y, small->y);
+            split(v.z, big->z, small->z);
+            split(v.w, big->w, small->w);
+        }
+        __syncthreads();
+    }
+    uint32_t q[S::kF32 ? 1 : D / 16][4];   // bf16: the warp's nodes, rows of Q as A fragments
+    // rows 0-7 / 8-15 of a fragment by chunk
+    const int qr = wm * 16 + (lane & 15), qc = lane >> 4;
+    if constexpr (!S::kF32) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) ldsm4(q[k], sq + S::at(wm * 16 + (lane & 15), 2 * k + (lane >> 4)));
+        for (int k = 0; k < D / 16; ++k) ldsm4(q[k], sq + S::at(qr, 2 * k + qc, q_rows));
+    }
     fence_async();     // Q's stage is a tile's next
     float o[D / 8][4];
 #pragma unroll
@@ -175,12 +233,11 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
     for (int t = 0; t < n_tiles; ++t) {
         const int f = fill0 + t;
         uint8_t *stage = ring + (f % kStages) * S::kStage;
-        if (bulk) ok = mbar_wait(&sh.full[f % kStages], (f / kStages) & 1, &sh.abort);
+        if (t < bulk) ok = mbar_wait(&sh.full[f % kStages], (f / kStages) & 1, &sh.abort);
         else cp_wait<kStages - 2>();
         const uint32_t sk = smem_u32(stage), sv = sk + S::kHalf;
-        const bool second = t >= tiles0;
-        const Keys &ks = parts[second ? 1 : 0];
-        const int k0 = (second ? t - tiles0 : t) * kTile;
+        int k0;
+        const Keys &ks = part_of(t, k0);
         // nodes mask each other; the window's first keys are out of the deeper
         // nodes' reach; with dedupe any of its keys may be in the dilated set
         const bool local = ks.kind != kSlab;
@@ -194,16 +251,16 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             for (int r = tid / S::kChunks; r < kTile; r += S::kRowsAtOnce) {
                 uint4 *e = v + S::at(r, tid % S::kChunks) / 16;
                 const uint4 x = *e;
-                if (not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w)) {
-                    __nv_bfloat16 *w = reinterpret_cast<__nv_bfloat16 *>(e);
+                if (not_finite<T>(x.x) || not_finite<T>(x.y) || not_finite<T>(x.z) || not_finite<T>(x.w)) {
+                    T *w = reinterpret_cast<T *>(e);
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i)
-                        if (!(fabsf(__bfloat162float(w[i])) < INFINITY)) w[i] = __float2bfloat16_rn(0.f);
+                    for (int i = 0; i < S::kPer; ++i)
+                        if (!(fabsf(value(w[i])) < INFINITY)) store1(w + i, 0.f);
                     sh.odd = 1;
                 }
             }
         }
-        if (bulk && k0 + kTile > ks.n) {
+        if (t < bulk && k0 + kTile > ks.n) {
             // rows behind the item's last hold anything: their values are zeroed
             uint4 *v = reinterpret_cast<uint4 *>(stage + S::kHalf);
 #pragma unroll 1
@@ -215,7 +272,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             if (tid == 0) {
                 report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
                 volatile int never = 0;
-                for (int q = f; q < fill0 + min(n_tiles, t + kStages - 1); ++q)   // copies in flight
+                for (int q = f; q < fill0 + min(bulk, t + kStages - 1); ++q)   // copies in flight
                     mbar_wait(&sh.full[q % kStages], (q / kStages) & 1, &never);
             }
             __syncthreads();
@@ -232,41 +289,70 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
         if (t + kStages - 1 < n_tiles) load(t + kStages - 1);
         cp_commit();
 #pragma unroll 1
-        for (int kb = wk; kb < kTile / 16; kb += WK) {
-            if (k0 + kb * 16 >= ks.n) break;
-            float s[2][4];
+        for (int kb = wk; kb < kTile / kBlock; kb += WK) {
+            if (k0 + kb * kBlock >= ks.n) break;
+            float s[NB][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[0][j] = s[1][j] = 0.f;
-            // lane's row of the four 8 x 8 matrices: keys 0-7 / 8-15 by chunk
-            const int kr = kb * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t f[4];
-                ldsm4(f, sk + S::at(kr, 2 * k + kc));
-                mma16816(s[0], q[k], f[0], f[1]);
-                mma16816(s[1], q[k], f[2], f[3]);
+                for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+            if constexpr (!S::kF32) {
+                // lane's row of the four 8 x 8 matrices: keys 0-7 / 8-15 by chunk
+                const int kr = kb * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t f[4];
+                    ldsm4(f, sk + S::at(kr, 2 * k + kc));
+                    mma16816(s[0], q[k], f[0], f[1]);
+                    mma16816(s[1], q[k], f[2], f[3]);
+                }
+            } else {
+                // two steps of 8 channels: four chunks of the block's 8 keys.  Each
+                // product of halves and each step has sums of its own: short chains
+                // of instructions, and few roundings of the instruction's (which cut)
+                const int kr = kb * 8 + (lane & 7), kc = lane >> 3;
+                float part[2][3][4] = {};
+#pragma unroll 2
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t f[4];
+                    ldsm4(f, sk + S::at(kr, 4 * k + kc));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t ab[4], as[4], bb[2], bs[2];
+                        ldsm4(ab, sq + S::at(qr, 4 * k + 2 * y + qc, q_rows));
+                        ldsm4(as, sq_small + S::at(qr, 4 * k + 2 * y + qc, q_rows));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) split(f[2 * y + i], bb[i], bs[i]);
+                        mma1688(part[y][0], ab, bb[0], bb[1]);
+                        mma1688(part[y][1], as, bb[0], bb[1]);
+                        mma1688(part[y][2], ab, bs[0], bs[1]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[0][j] = (part[0][0][j] + part[1][0][j]) + ((part[0][1][j] + part[1][1][j]) + (part[0][2][j] + part[1][2][j]));
             }
-            // s[n][2u + j]: node row r0 + 8u, key kb * 16 + 8n + c0 + j
-            float cnt[2][4];
+            // s[n][2u + j]: node row r0 + 8u, key kb * kBlock + 8n + c0 + j
+            float cnt[NB][4];
             if (masked) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int r = wm * 16 + r0 + 8 * u;
-                        const uint16_t w = r < n_nodes ? *reinterpret_cast<const uint16_t *>(&sh.count[r][kb * 16 + 8 * n + c0]) : (uint16_t)0;
+                        const uint16_t w = r < n_nodes ? *reinterpret_cast<const uint16_t *>(&sh.count[r][kb * kBlock + 8 * n + c0]) : (uint16_t)0;
                         cnt[n][2 * u] = (float)(w & 0xff);
                         cnt[n][2 * u + 1] = (float)(w >> 8);
                     }
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) cnt[n][j] = k0 + kb * 16 + 8 * n + c0 + (j & 1) < ks.n ? 1.f : 0.f;
+                    for (int j = 0; j < 4; ++j) cnt[n][j] = k0 + kb * kBlock + 8 * n + c0 + (j & 1) < ks.n ? 1.f : 0.f;
             }
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     s[n][j] = cnt[n][j] > 0.f ? s[n][j] * p.scale_log2 : -INFINITY;
@@ -293,22 +379,44 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             for (int u = 0; u < 2; ++u) {
                 const float ref = m[u] == -INFINITY ? 0.f : m[u];   // scores of -inf weigh nothing, NaN stays NaN
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int j = 2 * u; j < 2 * u + 2; ++j) {
                         s[n][j] = cnt[n][j] > 0.f ? cnt[n][j] * exp2f(s[n][j] - ref) : 0.f;
                         l[u] += s[n][j];
                     }
             }
-            const uint32_t pa[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
-                                    pack2(s[1][2], s[1][3])};
-            const int vr = kb * 16 + (lane & 15), vc = lane >> 4;
+            if constexpr (!S::kF32) {
+                const uint32_t pa[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[NB - 1][0], s[NB - 1][1]),
+                                        pack2(s[NB - 1][2], s[NB - 1][3])};
+                const int vr = kb * 16 + (lane & 15), vc = lane >> 4;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t f[4];
-                ldsm4t(f, sv + S::at(vr, 2 * i + vc));
-                mma16816(o[2 * i], pa, f[0], f[1]);
-                mma16816(o[2 * i + 1], pa, f[2], f[3]);
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t f[4];
+                    ldsm4t(f, sv + S::at(vr, 2 * i + vc));
+                    mma16816(o[2 * i], pa, f[0], f[1]);
+                    mma16816(o[2 * i + 1], pa, f[2], f[3]);
+                }
+            } else {
+                // the instruction's key index x is key 2 x, x + 4 key 2 x + 1: P's own order
+                uint32_t ab[4], as[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split(__float_as_uint(s[0][(i >> 1) + 2 * (i & 1)]), ab[i], as[i]);
+                const int vr = kb * 8 + c0;
+                const uint8_t *v = stage + S::kHalf + ((lane >> 2) & 3) * 4;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const int c = 2 * i + (lane >> 4);
+                    float t[4] = {};
+                    uint32_t bb[2], bs[2];
+                    split(*reinterpret_cast<const uint32_t *>(v + S::at(vr, c)), bb[0], bs[0]);
+                    split(*reinterpret_cast<const uint32_t *>(v + S::at(vr + 1, c)), bb[1], bs[1]);
+                    mma1688(t, as, bb[0], bb[1]);
+                    mma1688(t, ab, bs[0], bs[1]);
+                    mma1688(t, ab, bb[0], bb[1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[i][j] += t[j];
+                }
             }
         }
     }
@@ -346,13 +454,26 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             *reinterpret_cast<float2 *>(so + (warp * 16 + r) * D + (i * 8 + c0 + 8 * r) % D) = make_float2(o[i][2 * u] * w, o[i][2 * u + 1] * w);
     }
     __syncthreads();
-    const size_t base = ((size_t)b * p.slots_per_b + p.slot0[h] + slot) * p.N;
+    const size_t base = ((size_t)b * p.slots_per_b + p.head[h].slot0 + slot) * p.N;
+    const bool fused = p.head[h].fused != 0;
     if (wk == 0 && (lane & 3) == 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = wm * 16 + r0 + 8 * u;
-            if (r < n_nodes) p.ml[base + sh.nodes[r]] = make_float2(M[u], sh.bad ? -1.f : L[u]);
+            if (r >= n_nodes) continue;
+            if (!fused) {
+                p.ml[base + sh.nodes[r]] = make_float2(M[u], sh.bad ? -1.f : L[u]);
+            } else {
+                // the result itself: absent nodes and a pair with an invalid page are zero
+                const float sum = sh.bad || sh.ti.depth[r] < 0 ? 0.f : L[u];
+                sh.inv[r] = sum == 0.f ? 0.f : 1.f / sum;
+                if (p.lse) p.lse[((size_t)b * p.H + h) * p.N + r] = sum == 0.f ? -INFINITY : (M[u] + log2f(sum)) * 0.69314718055994531f;
+            }
         }
+    }
+    if (fused) {
+        if (sh.bad && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
+        __syncthreads();
     }
     if (sh.odd) {
         // the values left out: each reaches the nodes that see its key (the
@@ -365,10 +486,9 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
                 for (int i = 0; i < parts[part].n; ++i) {
                     const long long off = key_offset(p, parts[part], b, h, i);
                     if (off < 0) continue;
-                    const __nv_bfloat16 *v = parts[part].kind == kNodes
-                                                 ? static_cast<const __nv_bfloat16 *>(p.node_rows) + (size_t)p.N * D
-                                                 : static_cast<const __nv_bfloat16 *>(p.cache[1]);
-                    const float x = __bfloat162float(v[off + c]);
+                    const T *v = parts[part].kind == kNodes ? static_cast<const T *>(p.node_rows) + (size_t)p.N * D
+                                                            : static_cast<const T *>(p.cache[1]);
+                    const float x = value(v[off + c]);
                     if (fabsf(x) < INFINITY) continue;
 #pragma unroll 1
                     for (int n = 0; n < n_nodes; ++n)
@@ -387,29 +507,39 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             const float4 y = *reinterpret_cast<const float4 *>(src + k * WM * 16 * D);
             x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         }
-        *reinterpret_cast<float4 *>(p.part + (base + sh.nodes[r]) * D + c) = x;
+        if (!fused) {
+            *reinterpret_cast<float4 *>(p.part + (base + sh.nodes[r]) * D + c) = x;
+        } else {
+            const float w = sh.inv[r];   // 0: nothing to give, whatever the sums hold
+            x = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
+            IO4<T>::store(static_cast<T *>(p.o) + (((size_t)b * p.N + r) * p.H + h) * D + c, x);
+        }
     }
     return true;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 3) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     allow_next();
     const int b = blockIdx.x / p.ctas_per_b, it = blockIdx.x % p.ctas_per_b;
-    const int h = find_tree_head(p, it), li = it - p.cta0[h];
+    const int h = find_tree_head(p, it), li = it - p.head[h].cta0;
     const int pos = p.pos[b];
     if (tid == kThreads - 1) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1);
+        for (int i = 0; i < kStagesMax; ++i) mbar_init(&sh.full[i], 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     int fills = 0;
-    if (tid < 32) tree_analyse(sh.ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
-    else if (tid < 32 + kTreeMaxNodes) sh.parent[tid - 32] = tid - 32 < p.N ? p.parent[(size_t)b * p.N + tid - 32] : RAT_NODE_ABSENT;
+    if (tid < 32) {
+        tree_analyse(sh.ti, p.parent + (size_t)b * p.N, p.N, pos, p.cap);
+        __syncwarp();
+        if (li < p.head[h].wsplit) tree_masks(p, sh.ti, h, pos);
+    }
+    if (tid >= 32 && tid < 32 + kTreeMaxNodes) sh.parent[tid - 32] = tid - 32 < p.N ? p.parent[(size_t)b * p.N + tid - 32] : RAT_NODE_ABSENT;
     __syncthreads();
     if (li == 0) tell_pieces(p, sh.ti, b, h, pos);
     if (!sh.ti.valid || sh.ti.max_depth < 0) {
@@ -417,17 +547,17 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p, 
         if (blockIdx.x == gridDim.x - 1) wait_previous();
         return;
     }
-    const int ws = p.wsplit[h];
-    const int sets = tree_num_sets(p, p.dil[h], sh.ti.max_depth), items = sets * p.nsplit[h];
+    const int ws = p.head[h].wsplit;
+    const int sets = tree_num_sets(p, p.head[h].dil, sh.ti.max_depth), items = sets * p.head[h].nsplit;
     // CTAs below ws take one local item, the others slab items x, x + slab_ctas, ...
 #pragma unroll 1
-    for (int x = li < ws ? items - 1 : li - ws; x < items; x += max(1, p.slab_ctas[h])) {
-        Keys parts[2];
+    for (int x = li < ws ? max(items, 1) - 1 : li - ws; x < items; x += max(1, p.head[h].slab_ctas)) {
+        Keys parts[3];
         int n = 1, slot = x / sets;
         if (li < ws) {
-            slot = p.nsplit[h] + li;
+            slot = p.head[h].nsplit + li;
             n = local_keys(p, h, pos, li, parts);
-            if (li == 0) run_tree<__nv_bfloat16, D>(p, sh.parent, b, h, ring);
+            if (li == 0) run_tree<T, D>(p, sh.parent, b, h, reinterpret_cast<float *>(ring));
             if (tid == 0) sh.n = p.N;
             if (tid < p.N) sh.nodes[tid] = tid;
         } else {
@@ -435,31 +565,38 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(const TreeParams p, 
             __syncthreads();
             if (tid < 32) list_nodes(p, sh.ti, h, x % sets, sh.nodes, &sh.n);
         }
-        if (!run_item<D>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills)) break;
+        if (!run_item<T, D>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills)) break;
     }
     // this kernel ends after the one before it (tree_tc.cu's part of the step),
     // so that the one after, which waits for this one, has both
     if (blockIdx.x == gridDim.x - 1) wait_previous();
 }
 
-template <int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
-    constexpr size_t kRing = kStages * (size_t)Shape<D>::kStage;
-    static_assert(kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
-    const size_t smem = (kRing > tree_smem<D>(kTreeMaxNodes) ? kRing : tree_smem<D>(kTreeMaxNodes)) + 1024;
+template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
+    using S = Shape<T, D>;
+    static_assert(S::kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
+    static_assert(S::kTile <= kTileMax && S::kStages <= kStagesMax, "tile and ring as declared");
+    const size_t ring = S::kRing + (S::kF32 ? (size_t)padded_nodes(p.N) * D * 2 * sizeof(T) : 0), tree = tree_smem(p.N, p.sep);
+    const size_t smem = (ring > tree ? ring : tree) + 1024;   // bf16: three CTAs an SM
     static std::atomic<unsigned long long> smem_set{0};
-    cudaError_t e = ensure_smem_limit(tree_mma_kernel<D>, smem, smem_set);
+    // the limit is raised once per device, so to the largest tree's
+    const size_t most = S::kRing + (S::kF32 ? (size_t)kTreeMaxNodes * D * 8 : 0), most_tree = tree_smem(kTreeMaxNodes, 1);
+    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D>, (most > most_tree ? most : most_tree) + 1024, smem_set);
     if (e != cudaSuccess) return e;
     Maps maps = {};
     if (!p.page_table)
         for (int x = 0; x < 2; ++x)
-            if (!encode_map_rows(&maps.kv[x], p.cache[x], p.cache_R, (long long)p.B * p.H, D, kTile)) return cudaErrorInvalidValue;
-    return launch_after(tree_mma_kernel<D>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
+            if (!encode_map_rows(&maps.kv[x], p.cache[x], sizeof(T) == 4 ? RAT_F32 : RAT_BF16, p.cache_R, (long long)p.B * p.H, D, S::kTile))
+                return cudaErrorInvalidValue;
+    return launch_after(tree_mma_kernel<T, D>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_mma(const TreeParams &p, unsigned grid, cudaStream_t s) {
-    return p.d == 128 ? launch_typed<128>(p, grid, s) : launch_typed<64>(p, grid, s);
+cudaError_t launch_tree_mma(const TreeParams &p, int dtype, unsigned grid, cudaStream_t s) {
+    if (dtype == RAT_BF16)
+        return p.d == 128 ? launch_typed<__nv_bfloat16, 128>(p, grid, s) : launch_typed<__nv_bfloat16, 64>(p, grid, s);
+    return p.d == 128 ? launch_typed<float, 128>(p, grid, s) : launch_typed<float, 64>(p, grid, s);
 }
 
 }  // namespace rat

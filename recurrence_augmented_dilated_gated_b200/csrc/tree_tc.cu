@@ -418,7 +418,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
 #pragma unroll
             for (int n = 0; n < (NP + 31) / 32; ++n) sh.part[warp][lane * NP / 32 + n] = l[n];
             if (!(ok = sync())) break;
-            const size_t rowbase = ((size_t)b * p.slots_per_b + p.slot0[h] + slot) * p.N;
+            const size_t rowbase = ((size_t)b * p.slots_per_b + p.head[h].slot0 + slot) * p.N;
             ok = mbar_wait(&sh.copied[items & 3], (items >> 2) & 1, &sh.abort) && mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -461,7 +461,7 @@ template <int NP> cudaError_t launch_np(const TreeParams &p, cudaStream_t s) {
     const long long rows = p.page_table ? p.page_rows : p.cache_R, blocks = (long long)(p.page_table ? p.num_pages : p.B) * p.H;
     maps.box = p.page_table && p.page_rows < kTile ? p.page_rows : kTile;
     for (int x = 0; x < 2; ++x)
-        if (!encode_map_rows(&maps.kv[x], p.cache[x], rows, blocks, kD, maps.box)) return cudaErrorInvalidValue;
+        if (!encode_map_rows(&maps.kv[x], p.cache[x], RAT_BF16, rows, blocks, kD, maps.box)) return cudaErrorInvalidValue;
     const long long total = (long long)p.B * p.tc_items_per_b;
     tree_tc_kernel<NP><<<(unsigned)(total < 148 ? total : 148), kThreads, kBytes + 1024, s>>>(p, maps);
     return cudaGetLastError();

@@ -80,6 +80,35 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// two floats at once (f32x2 arithmetic: one instruction for both)
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// The softmax warps' barrier.  None of them leaves its loop early, however a
+// wait ended, so every one of them comes here as often.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r) : "r"((uint32_t)x), "n"(kSoftmax) : "memory");
+    return r != 0;
+}
+
 // The items of a CTA, in order; every role walks the same list.
 struct Items {
     int u, b, h, slot, tiles;
@@ -106,13 +135,12 @@ struct Items {
 };
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots], sfull[2], sempty[2], qfull, pfull, pvdone, copied[4], soft, drain;
+    uint64_t full[kSlots], empty[kSlots], sfull[2], sempty[2], qfull, pfull, pvdone, copied[4], drain;
     uint32_t tmem;
     volatile int abort;
     int bad[4];                       // item number + 1 of an item with an invalid page, by item mod 4 (the copies
                                       // run at most three items ahead of the softmax, as does copied)
-    volatile int over[2];             // tile number + 1 when a reference has to be raised, by tile mod 2
-    alignas(16) float ref[kTreeMaxNodes];   // read four at a time
+    alignas(16) float nref[kTreeMaxNodes];  // the references, negative; read four at a time
     float corr[kTreeMaxNodes];
     float part[4][kTreeMaxNodes];     // a warp's maxima or sums
 };
@@ -158,11 +186,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         mbar_init(&sh.pfull, kSoftmax);
         mbar_init(&sh.pvdone, 1);
         for (int i = 0; i < 4; ++i) mbar_init(&sh.copied[i], 32);
-        mbar_init(&sh.soft, kSoftmax);
         mbar_init(&sh.drain, 1);
         sh.abort = 0;
         for (int i = 0; i < 4; ++i) sh.bad[i] = 0;
-        sh.over[0] = sh.over[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 5) {
@@ -272,11 +298,12 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         // ------------------------------------------------ softmax
         constexpr int kCols = NP < 32 ? NP : 32;   // columns of O at a time
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
-        int t_all = 0, items = 0, syncs = 0;
-        // all softmax warps (a bounded wait, so that a warp that gave up strands no other)
-        auto sync = [&]() {
-            mbar_arrive(&sh.soft);
-            return __all_sync(0xffffffffu, mbar_wait(&sh.soft, syncs++ & 1, &sh.abort)) != 0;
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+        int t_all = 0, items = 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (__all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort))) return;
+            ok = false;
+            sh.abort = 1;   // the waits that follow, everyone's, end at once
         };
         // queries of an item: row n of Q is node n (absent nodes: zeros)
         auto stage_q = [&](int b, int h) {
@@ -292,62 +319,73 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         };
         bool more = it.next(p, total);
         if (more) stage_q(it.b, it.h);
-        while (ok && more) {
-            float l[NP];
+        while (more) {
+            uint64_t l2[NP / 2];
 #pragma unroll
-            for (int n = 0; n < NP; ++n) l[n] = 0.f;
+            for (int n = 0; n < NP / 2; ++n) l2[n] = 0ull;
             for (int t = 0; t < it.tiles; ++t, ++t_all) {
-                ok = mbar_wait(&sh.sfull[t_all & 1], (t_all / 2) & 1, &sh.abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                wait(&sh.sfull[t_all & 1], (t_all / 2) & 1);
                 tc_after();
-                uint32_t s[NP];
-                ld_cols<NP>(t_lane + (t_all & 1) * 64, s);
-                tc_before();
-                mbar_arrive(&sh.sempty[t_all & 1]);
                 const bool valid = t * kTile + tid < it.ks.n;
-                bool over = t == 0;
-                if (!over) {
-                    float mx = -INFINITY;
+                // x = score * scale - reference, in the log2 domain
+                uint64_t x2[NP / 2];
+                auto scores = [&]() {
+                    uint32_t s[NP];
+                    ld_cols<NP>(t_lane + (t_all & 1) * 64, s);
 #pragma unroll
                     for (int n = 0; n < NP; n += 4) {
-                        const float4 r = *reinterpret_cast<const float4 *>(&sh.ref[n]);
-                        mx = fmaxf(mx, fmaxf(fmaxf(fmaf(__uint_as_float(s[n]), p.scale_log2, -r.x), fmaf(__uint_as_float(s[n + 1]), p.scale_log2, -r.y)),
-                                             fmaxf(fmaf(__uint_as_float(s[n + 2]), p.scale_log2, -r.z), fmaf(__uint_as_float(s[n + 3]), p.scale_log2, -r.w))));
+                        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(&sh.nref[n]);
+                        x2[n / 2] = fma2(pack2(__uint_as_float(s[n]), __uint_as_float(s[n + 1])), scale2, r.x);
+                        x2[n / 2 + 1] = fma2(pack2(__uint_as_float(s[n + 2]), __uint_as_float(s[n + 3])), scale2, r.y);
+                    }
+                };
+                bool over = t == 0;
+                if (!over) {
+                    scores();
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < NP / 2; ++n) {
+                        float a, c;
+                        unpack2(x2[n], a, c);
+                        mx = fmaxf(mx, fmaxf(a, c));
                     }
                     over = valid && mx > kSlack;
                 }
-                if (over) sh.over[t_all & 1] = t_all + 1;
-                if (!(ok = sync())) break;
-                if (sh.over[t_all & 1] == t_all + 1) {
+                if (softmax_any(over)) {
                     // some reference is raised (the first tile sets all of them):
                     // maxima over the tile's keys, by the integers in the floats' order
+                    {
+                        uint32_t s[NP];
+                        ld_cols<NP>(t_lane + (t_all & 1) * 64, s);
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) {
-                        const float x = __uint_as_float(s[n]) * p.scale_log2;
-                        int i = __float_as_int(valid && x == x ? x : -INFINITY);
-                        i ^= (i >> 31) & 0x7fffffff;
-                        i = __reduce_max_sync(0xffffffffu, i);
-                        i ^= (i >> 31) & 0x7fffffff;
-                        if (lane == (n & 31)) sh.part[warp][n] = __int_as_float(i);
+                        for (int n = 0; n < NP; ++n) {
+                            const float x = __uint_as_float(s[n]) * p.scale_log2;
+                            int i = __float_as_int(valid && x == x ? x : -INFINITY);
+                            i ^= (i >> 31) & 0x7fffffff;
+                            i = __reduce_max_sync(0xffffffffu, i);
+                            i ^= (i >> 31) & 0x7fffffff;
+                            if (lane == (n & 31)) sh.part[warp][n] = __int_as_float(i);
+                        }
                     }
-                    if (!(ok = sync())) break;
+                    softmax_sync();
                     if (tid < NP) {
                         float mx = fmaxf(fmaxf(sh.part[0][tid], sh.part[1][tid]), fmaxf(sh.part[2][tid], sh.part[3][tid]));
                         if (mx == -INFINITY) mx = 0.f;   // nothing but scores of -inf: they weigh nothing
-                        const float old = sh.ref[tid];
+                        const float old = -sh.nref[tid];
                         const bool up = t == 0 || mx > old + kSlack;
                         sh.corr[tid] = t > 0 && up ? exp2f(old - mx) : 1.f;
-                        if (up) sh.ref[tid] = mx;
+                        if (up) sh.nref[tid] = -mx;
                     }
-                    if (!(ok = sync())) break;
+                    softmax_sync();
                     if (t > 0) {
-#pragma unroll
-                        for (int n = 0; n < NP; ++n) l[n] *= sh.corr[n];
-                        ok = mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
+                        wait(&sh.pvdone, (t_all - 1) & 1);
                         tc_after();
+#pragma unroll
+                        for (int n = 0; n < NP; n += 2) {
+                            float a, c;
+                            unpack2(l2[n / 2], a, c);
+                            l2[n / 2] = pack2(a * sh.corr[n], c * sh.corr[n + 1]);
+                        }
 #pragma unroll 1
                         for (int n = 0; n < NP; n += kCols) {
                             uint32_t o[kCols];
@@ -356,38 +394,38 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                             for (int i = 0; i < kCols; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.corr[n + i]);
                             st_cols<kCols>(t_lane + 128 + n, o);
                         }
-                        tc_before();
                     }
+                    scores();
                 }
-                if (t_all > 0) {   // P of the tile before has been read
-                    ok = mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                tc_before();
+                mbar_arrive(&sh.sempty[t_all & 1]);
+                const bool tail = t == it.tiles - 1 && it.ks.n % kTile != 0;
+                if (tail && !valid) {
+#pragma unroll
+                    for (int n = 0; n < NP / 2; ++n) x2[n] = pack2(-INFINITY, -INFINITY);
                 }
+                if (t_all > 0) wait(&sh.pvdone, (t_all - 1) & 1);   // P of the tile before has been read
                 uint8_t *row = smem + kOffP + tid * 128;
 #pragma unroll
                 for (int n = 0; n < NP; n += 8) {
-                    const float4 ra = *reinterpret_cast<const float4 *>(&sh.ref[n]), rb = *reinterpret_cast<const float4 *>(&sh.ref[n + 4]);
-                    const float r[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
                     uint32_t pk[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        float a = ex2(fmaf(__uint_as_float(s[n + i]), p.scale_log2, -r[i]));
-                        float c = ex2(fmaf(__uint_as_float(s[n + i + 1]), p.scale_log2, -r[i + 1]));
-                        if (!valid) a = c = 0.f;
-                        l[n + i] += a;
-                        l[n + i + 1] += c;
+                        float a, c;
+                        unpack2(x2[(n + i) / 2], a, c);
+                        a = ex2(a);
+                        c = ex2(c);
+                        l2[(n + i) / 2] = add2(l2[(n + i) / 2], pack2(a, c));
                         __nv_bfloat162 v = __floats2bfloat162_rn(a, c);
                         pk[i / 2] = *reinterpret_cast<uint32_t *>(&v);
                     }
                     *reinterpret_cast<uint4 *>(row + (((n >> 3) ^ (tid & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
-                if (t == it.tiles - 1 && it.ks.n % kTile != 0) {
+                if (tail) {
                     // rows behind the item's last hold anything: their values are
                     // zeroed, as a probability of zero does not undo a NaN
                     const int v = 2 * t_all + 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[v % kSlots], (v / kSlots) & 1, &sh.abort));
-                    if (!ok) break;
+                    wait(&sh.full[v % kSlots], (v / kSlots) & 1);
                     if (!valid) {
                         uint4 *x = reinterpret_cast<uint4 *>(smem + (v % kSlots) * kSlot + tid * 128);
 #pragma unroll
@@ -397,13 +435,15 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                 fence_async();
                 mbar_arrive(&sh.pfull);
             }
-            if (!ok) break;
             // the item's last scores are in, so Q is free: the next item's go there
             const int b = it.b, h = it.h, slot = it.slot;
             more = it.next(p, total);
             if (more) stage_q(it.b, it.h);
             // sums over the keys: halves of the nodes change lanes until a lane
             // holds NP / 32 nodes' sums over its warp (or two lanes one node's)
+            float l[NP];
+#pragma unroll
+            for (int n = 0; n < NP; n += 2) unpack2(l2[n / 2], l[n], l[n + 1]);
 #pragma unroll
             for (int half = NP / 2, off = 16; off > 0; half >>= 1, off >>= 1) {
                 const bool up = lane & off;
@@ -417,15 +457,14 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             // lane bits, highest first, chose the halves: lane i holds nodes i * NP / 32 ...
 #pragma unroll
             for (int n = 0; n < (NP + 31) / 32; ++n) sh.part[warp][lane * NP / 32 + n] = l[n];
-            if (!(ok = sync())) break;
+            softmax_sync();
             const size_t rowbase = ((size_t)b * p.slots_per_b + p.head[h].slot0 + slot) * p.N;
-            ok = mbar_wait(&sh.copied[items & 3], (items >> 2) & 1, &sh.abort) && mbar_wait(&sh.pvdone, (t_all - 1) & 1, &sh.abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            wait(&sh.copied[items & 3], (items >> 2) & 1);
+            wait(&sh.pvdone, (t_all - 1) & 1);
             if (tid < p.N) {
                 const float sum = (sh.part[0][tid] + sh.part[1][tid]) + (sh.part[2][tid] + sh.part[3][tid]);
                 const bool bad = *(volatile int *)&sh.bad[items & 3] == items + 1;
-                p.ml[rowbase + tid] = make_float2(sum == 0.f ? -INFINITY : sh.ref[tid], bad ? -1.f : sum);
+                p.ml[rowbase + tid] = make_float2(sum == 0.f ? -INFINITY : -sh.nref[tid], bad ? -1.f : sum);
             }
             ++items;
             tc_after();
@@ -438,12 +477,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                     if (n + i < p.N) p.part[(rowbase + n + i) * kD + tid] = __uint_as_float(o[i]);
             }
             tc_before();
-            ok = sync();   // sh.ref and sh.part are read
+            softmax_sync();   // sh.nref and sh.part are read
         }
-        if (!ok) {
-            sh.abort = 1;
-            if (lane == 0) report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
-        }
+        if (!ok && lane == 0) report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
     }
     tc_before();
     __syncthreads();

@@ -39,7 +39,8 @@ def fill(cfg, cap, hist, pos):
     """A cache [B,H,R,d] holding the rows of positions < pos[b] of hist [B,cap,H,d]; every other row is NaN."""
     c = cfg.c
     R = rat.rat_cache_rows(cfg, cap)
-    cache = torch.full((c.B, c.H, R, c.d), float("nan"), dtype=hist.dtype)
+    cache = torch.full((c.B, c.H, R, c.d), float("nan"), dtype=hist.dtype, device=DEV)
+    hist = hist.to(DEV)
     for h in range(c.H):
         for b in range(c.B):
             main, ring = {}, {}
@@ -52,7 +53,7 @@ def fill(cfg, cap, hist, pos):
             for rows in (main, ring):
                 if rows:
                     cache[b, h, list(rows)] = hist[b, list(rows.values()), h]
-    return cache.to(DEV)
+    return cache
 
 
 def random_parents(rng, B, N, max_depth, pad=True):
@@ -210,6 +211,108 @@ def test_long_context_in_many_pieces(dtype):
     p.check(*p.step())
 
 
+#: heads whose nodes all read the same rows, in a cache large enough (2^20 such rows by capacity) for the tcgen05
+#: form: (dil, win, grid, N, cap, positions, max depth)
+LARGE = [
+    ([1, 1], [0, 0], 0, 1, 530000, [1], 1),
+    ([1, 4], [0, 30], 0, 8, 600000, [0, 127], 4),
+    ([1, 3], [20, 0], 0, 16, 350000, [128, 129, 1], 5),
+    ([1, 64], [0, 200], 0, 17, 550000, [2500, 640], 6),
+    ([2, 5], [40, 0], 1, 33, 800000, [3001, 255], 9),
+    ([1, 1], [0, 7], 0, 64, 300000, [1000, 4700], 12),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LARGE)))
+@pytest.mark.parametrize("page_rows", [0, 8, 64, 128, 384, 40])
+def test_large_capacities(case, page_rows):
+    # dense, in pages that the tcgen05 form copies (parts and multiples of 128 rows) and in others
+    dil, win, grid, N, cap, pos, deep = LARGE[case]
+    cfg = config(len(pos), N, len(dil), 128, BF16, dil, win, [0] + [1] * (len(dil) - 1), grid)
+    p = Problem(cfg, cap, pos, random_parents(np.random.default_rng(case), len(pos), N, deep), seed=case).to_gpu()
+    if not page_rows:
+        p.check(*p.step())
+        return
+    _, _, desc = short_pages(cfg, cap, p, page_rows)
+    p.check(*p.step(desc))
+
+
+def short_pages(cfg, cap, p, page_rows):
+    """Pages for the rows that the positions held and the tree need only; the table's other entries are -1."""
+    c = cfg.c
+    R = p.ck.shape[2]
+    pps = -(-R // page_rows)
+    table = np.full((c.B, pps), -1, np.int32)
+    n = 0
+    for b in range(c.B):
+        used = set()
+        for h in range(c.H):
+            for j in range(p.pos[b] + c.T):
+                used |= {r // page_rows for r in rows_of(cfg, cap, h, j) if r >= 0}
+        for i in sorted(used):
+            table[b, i] = n
+            n += 1
+    table[table >= 0] = np.random.default_rng(3).permutation(n)[table[table >= 0]]
+    pools = []
+    for x in (p.ck, p.cv):
+        pool = torch.full((max(n, 1), c.H, page_rows, c.d), float("nan"), dtype=x.dtype, device=DEV)
+        for b, i in zip(*np.nonzero(table >= 0)):
+            rows = x[b, :, i * page_rows:(i + 1) * page_rows]
+            pool[int(table[b, i]), :, :rows.shape[1]] = rows
+        pools.append(pool)
+    d_table = torch.from_numpy(table).to(DEV)
+    return pools, d_table, rat.paged_cache(cfg, pools[0], pools[1], d_table, cap)
+
+
+@pytest.mark.parametrize("page_rows", [64, 128])
+def test_an_invalid_page_of_a_large_capacity(page_rows):
+    cfg = config(3, 20, 2, 128, BF16, [1, 8], [0, 12])
+    p = Problem(cfg, 400000, [1000, 700, 900], random_parents(np.random.default_rng(4), 3, 20, 5, pad=False)).to_gpu()
+    want = p.step()
+    _, table, desc = short_pages(cfg, p.cap, p, page_rows)
+    got = p.step(desc)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    table[1, 512 // page_rows] = -1            # rows 512 ..: head 0's positions; head 1 has none there (its slab is 50000)
+    o, lse = p.step(desc, check=False)
+    with pytest.raises(rat.RatError, match="RAT_ERR_INVALID"):
+        rat.rat_check_status(p.ws)
+    assert torch.all(o[1, :, 0] == 0) and torch.all(torch.isneginf(lse[1, 0]))
+    assert torch.equal(o[1, :, 1], want[0][1, :, 1]) and torch.equal(o[[0, 2]], want[0][[0, 2]])
+    table[1, 512 // page_rows] = int(table.max()) + 1
+    o2, _ = p.step(desc, check=False)
+    assert torch.equal(o2, o)
+    with pytest.raises(rat.RatError, match="RAT_ERR_INVALID"):
+        rat.rat_check_status(p.ws)
+
+
+def test_scores_that_outgrow_the_first_tile():
+    # the references are set by an item's first keys and have to be raised by later ones, in every form of the step:
+    # keys grow along the sequence until their scores are hundreds above the first
+    for cap, dtype, d in ((600000, BF16, 128), (4000, BF16, 128), (4000, F32, 128), (4000, BF16, 64)):
+        cfg = config(2, 24, 1, d, dtype, [1], [0], scale=1.0)
+        p = Problem(cfg, cap, [1900, 1030], random_parents(np.random.default_rng(6), 2, 24, 6, pad=False))
+        ramp = torch.linspace(0.01, 6.0, p.hk.shape[1])[None, :, None, None]
+        p.hk = (p.hk.float() * ramp).to(dtype)
+        p.to_gpu()
+        p.check(*p.step())
+
+
+def test_large_step_next_to_another_and_repeated():
+    # two steps of the persistent form at once, each with its own workspace, then the same bits again
+    cfg = config(2, 40, 2, 128, BF16, [1, 1], [0, 30])
+    ps = [Problem(cfg, 280000, [5000, 3333], random_parents(np.random.default_rng(i), 2, 40, 6), seed=i).to_gpu()
+          for i in range(2)]
+    want = [p.step() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [p.step(stream=s, check=False) for p, s in zip(ps, streams)]
+        torch.cuda.synchronize()
+        for g, w, p in zip(got, want, ps):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+            rat.rat_check_status(p.ws)
+
+
 def test_custom_scale_and_no_lse():
     cfg = config(2, 9, 2, 64, BF16, [2, 1], [0, 6], scale=0.3)
     p = Problem(cfg, 300, [250, 5], random_parents(np.random.default_rng(1), 2, 9, 4)).to_gpu()
@@ -344,14 +447,16 @@ def test_an_invalid_page_skips_its_pair(dtype, entry, part):
     assert torch.equal(o[1, :, 0], want[0][1, :, 0])     # head 0 holds positions < 150 only: rows below 150
 
 
-def test_pages_far_into_a_large_pool():
+@pytest.mark.parametrize("cap", [128, 140000])
+def test_pages_far_into_a_large_pool(cap):
     # element offsets past 2^32 in a pool of 17 GB; two pages of it are used
     cfg = config(1, 5, 8, 128, BF16, [1] * 8, [0] * 8)
-    p = Problem(cfg, 128, [120], random_parents(np.random.default_rng(2), 1, 5, 3)).to_gpu()
+    p = Problem(cfg, cap, [120], random_parents(np.random.default_rng(2), 1, 5, 3)).to_gpu()
     want = p.step()
     n = (1 << 32) // (8 * 64 * 128) + 9
     pools = [torch.empty(n, 8, 64, 128, dtype=BF16, device=DEV) for _ in range(2)]
-    table = torch.tensor([[n - 1, n - 5]], dtype=torch.int32, device=DEV)
+    table = torch.full((1, -(-p.ck.shape[2] // 64)), -1, dtype=torch.int32, device=DEV)
+    table[0, 0], table[0, 1] = n - 1, n - 5
     for pool, x in zip(pools, (p.ck, p.cv)):
         for i in range(2):
             pool[int(table[0, i])] = x[0, :, 64 * i:64 * i + 64]

@@ -30,7 +30,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;
+constexpr int kSmall = 8, kLarge = 16;   // CTAs of the cluster
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
@@ -51,12 +51,12 @@ __device__ __forceinline__ bool page_needed(const HeadClass &c, int grid, unsign
 
 constexpr int kHeld = 16;   // entries of a run that a lane keeps in registers between the sweeps
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) page_update_kernel(const PageUpdateParams p) {
+__global__ void __launch_bounds__(kThreads, 1) page_update_kernel(const PageUpdateParams p) {
     __shared__ int s_cnt[2][kWarps];       // entries of each warp that give / take a page
     __shared__ int s_sum[2];               // and of the CTA
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = (int)cluster.block_rank();
+    const int rank = (int)cluster.block_rank(), kCluster = (int)cluster.num_blocks();
     const int total = p.B * p.pps;         // < 2^31
     const int run = (int)((((long long)total + kCluster * kWarps - 1) / (kCluster * kWarps) + 31) & ~31LL);
     const long long lo = (long long)(rank * kWarps + warp) * run;
@@ -129,17 +129,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
         if (lane == 31) s_sum[warp] = x;
     }
     cluster.sync();
+    // a lane reads one CTA's sums
     int give0 = s_cnt[0][warp], take0 = s_cnt[1][warp], gives = 0, takes = 0;
-    for (int r = 0; r < kCluster; ++r) {
-        const int *sum = cluster.map_shared_rank(s_sum, r);
-        const int g = sum[0], t = sum[1];
-        gives += g;
-        takes += t;
-        if (r < rank) {
-            give0 += g;
-            take0 += t;
-        }
+    if (lane < kCluster) {
+        const int *sum = cluster.map_shared_rank(s_sum, lane);
+        gives = sum[0];
+        takes = sum[1];
     }
+    give0 += __reduce_add_sync(0xffffffffu, lane < rank ? gives : 0);
+    take0 += __reduce_add_sync(0xffffffffu, lane < rank ? takes : 0);
+    gives = __reduce_add_sync(0xffffffffu, gives);
+    takes = __reduce_add_sync(0xffffffffu, takes);
     // a stack that cannot be right (more pages given back than there are) is left alone
     const bool ok = n_free >= 0 && (long long)n_free + gives <= p.num_pages;
     const int top = n_free + gives;
@@ -148,22 +148,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
         if (st == 1) p.free_pages[n_free + give0 + __popc(m & below)] = page;
         give0 += __popc(m);
     };
-    auto settle = [&](int st, int e) {
+    // the stack's place for an entry that takes a page, -1 when it ran out
+    auto place = [&](int st) {
         const unsigned m = __ballot_sync(0xffffffffu, st == 2);
-        if (e < e_hi && st == 2) {
-            const int at = top - 1 - (take0 + __popc(m & below));
-            int got = at >= 0 ? __ldcg(p.free_pages + at) : -1;
-            if (at < 0) {
-                report_error(p.hdr, RAT_ERR_NO_PAGES, (int)p.by_pps.div(e));
-            } else if (got < 0 || got >= p.num_pages) {
-                got = -1;
-                report_error(p.hdr, RAT_ERR_INVALID, (int)p.by_pps.div(e));
-            }
-            p.table[e] = got;
-        } else if (e < e_hi && st != 3) {
-            p.table[e] = -1;
-        }
+        const int at = top - 1 - (take0 + __popc(m & below));
         take0 += __popc(m);
+        return st == 2 && at >= 0 ? at : -1;
+    };
+    auto settle = [&](int st, int e, int at, int got) {
+        if (e >= e_hi || st == 3) return;
+        if (st != 2) {
+            p.table[e] = -1;
+            return;
+        }
+        if (at < 0) report_error(p.hdr, RAT_ERR_NO_PAGES, (int)p.by_pps.div(e));
+        if (at >= 0 && (got < 0 || got >= p.num_pages)) {
+            got = -1;
+            report_error(p.hdr, RAT_ERR_INVALID, (int)p.by_pps.div(e));
+        }
+        p.table[e] = got;
     };
     if (ok) {
 #pragma unroll
@@ -179,13 +182,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
     }
     cluster.sync();   // the pages given back are on the stack
     if (ok) {
-#pragma unroll 4
+        // a lane's pages are fetched together
+        int at[kHeld], got[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) at[i] = place((states >> (2 * i)) & 3);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) got[i] = at[i] >= 0 ? __ldcg(p.free_pages + at[i]) : -1;
+#pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             if (e_lo + i * 32 >= e_hi) break;
-            settle((states >> (2 * i)) & 3, e_lo + i * 32 + lane);
+            settle((states >> (2 * i)) & 3, e_lo + i * 32 + lane, at[i], got[i]);
         }
 #pragma unroll 1
-        for (int e = e_more; e < e_hi; e += 32) settle(e + lane < e_hi ? look(e + lane, page) : 0, e + lane);
+        for (int e = e_more; e < e_hi; e += 32) {
+            const int st = e + lane < e_hi ? look(e + lane, page) : 0, where = place(st);
+            settle(st, e + lane, where, where >= 0 ? __ldcg(p.free_pages + where) : -1);
+        }
         for (int b = rank * kThreads + tid; b < p.B; b += kCluster * kThreads)
             if (p.length[b] > p.cap) report_error(p.hdr, RAT_ERR_INVALID, b);
     }
@@ -245,6 +257,16 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
         }
         __syncthreads();
         const size_t out0 = ((size_t)b * p.T + i0) * p.H;
+        if (p.ncls <= kSlotClasses && p.H % 2 == 0) {
+            // two heads of a position at a time: 16-byte stores
+            auto value = [&](long long at, int h) { return at < 0 ? -1 : at + h * stride; };
+            for (int e = 2 * tid; e < nt * p.H; e += 2 * kSlotThreads) {
+                const int i = p.by_h.div(e), h = e - i * p.H, a = i * nc + s_cls[h], c = i * nc + s_cls[h + 1];
+                *reinterpret_cast<longlong2 *>(p.slots + out0 + e) = make_longlong2(value(s_at[0][a], h), value(s_at[0][c], h + 1));
+                if (p.ring) *reinterpret_cast<longlong2 *>(p.ring + out0 + e) = make_longlong2(value(s_at[1][a], h), value(s_at[1][c], h + 1));
+            }
+            continue;
+        }
         for (int e = tid; e < nt * p.H; e += kSlotThreads) {
             const int i = p.by_h.div(e), h = e - i * p.H, c = s_cls[h] - c0;
             if (c < 0 || c >= nc) continue;
@@ -261,7 +283,36 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
 }  // namespace
 
 cudaError_t launch_page_update(const PageUpdateParams &p, cudaStream_t s) {
-    page_update_kernel<<<kCluster, kThreads, 0, s>>>(p);
+    // sixteen CTAs (not a portable size) for a table that eight would hold in more
+    // than kHeld / 2 entries a lane, where the device can place them
+    static std::atomic<int> large{-1};
+    int size = kSmall;
+    if ((long long)p.B * p.pps > (long long)kSmall * kThreads * (kHeld / 2)) size = kLarge;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (size == kLarge) {
+        int can = large.load(std::memory_order_acquire);
+        if (can < 0) {
+            cfg.gridDim = dim3(kLarge);
+            attr.val.clusterDim.x = kLarge;
+            int n = 0;
+            can = cudaFuncSetAttribute(page_update_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&n, page_update_kernel, &cfg) == cudaSuccess && n > 0;
+            if (!can) cudaGetLastError();
+            large.store(can, std::memory_order_release);
+        }
+        if (!can) size = kSmall;
+    }
+    cfg.gridDim = dim3(size);
+    attr.val.clusterDim.x = size;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, page_update_kernel, p);
+    if (e != cudaSuccess) return e;
     count_launches(1);
     return cudaGetLastError();
 }

@@ -190,7 +190,7 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
             nodes = k < n_sets ? (N + sets_of(dils[0][k]) - 1) / sets_of(dils[0][k]) : N;
         }
     const int fixed = (c->dtype == RAT_BF16 ? 640 : 160) / (nodes <= 16 ? 1 : nodes <= 32 ? 2 : 4);
-    const int target = piece_target(kinds[0], n_kinds[0], c->B, 3 * kSMs, fixed);
+    const int target = piece_target(kinds[0], n_kinds[0], c->B, (c->dtype == RAT_BF16 ? 3 : 2) * kSMs, fixed);
     const int window_rows = target > 128 ? target : 128;
     // A CTA that takes several items looks at the tree once: not many more CTAs than
     // twelve rounds of them, however many items there are.

@@ -57,8 +57,10 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
 }
 // x = big + small, big with the 11 bits of tf32 (the instruction cuts small to as many)
 __device__ __forceinline__ void split(uint32_t x, uint32_t &big, uint32_t &small) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(big) : "f"(__uint_as_float(x)));
-    small = __float_as_uint(__uint_as_float(x) - __uint_as_float(big));
+    uint32_t b;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(b) : "f"(__uint_as_float(x)));
+    small = __float_as_uint(__uint_as_float(x) - __uint_as_float(b));
+    big = b;
 }
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
@@ -95,8 +97,10 @@ struct Maps {
     CUtensorMap kv[2];
 };
 
-// Rows of Q that the warps read: 16 for one, two or four of them.
+// Rows of Q that the warps read: 16 for one, two or four of them; and the bytes of
+// an fp32 Q, in halves for up to 32 nodes.
 __host__ __device__ __forceinline__ int padded_nodes(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : 64; }
+template <int D> constexpr size_t q_bytes(int n) { return (size_t)(n <= 16 ? 16 : 32) * D * 8; }
 
 struct Shared {
     TreeInfo ti;
@@ -141,9 +145,12 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
     fills += bulk;
 
     // Q: into the stage that no tile uses yet (bf16: it goes on to registers), or
-    // a place of its own (fp32: in halves it would be 128 registers)
+    // a place of its own (fp32: in halves it would be 128 registers; the halves of
+    // up to 32 nodes are made once, those of 64 nodes as they are used, so that
+    // the place stays within 32 KB and two CTAs within an SM)
     const uint32_t sq = smem_u32(ring) + (S::kF32 ? S::kRing : ((fill0 + kStages - 1) % kStages) * S::kStage);
-    const int q_rows = S::kF32 ? padded_nodes(p.N) : kTreeMaxNodes;   // >= 16 WM
+    const int q_rows = S::kF32 ? 16 * WM : kTreeMaxNodes;
+    const bool halves = S::kF32 && WM < 4;
     for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
         const int r = e / S::kChunks, c = e % S::kChunks;
         const bool on = r < n_nodes;
@@ -201,7 +208,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
     cp_wait<kStages - 1>();
     __syncthreads();
     const uint32_t sq_small = sq + q_rows * D * 4;   // fp32: Q in halves, the small ones behind the big
-    if constexpr (S::kF32) {
+    if (halves) {
         uint4 *x = reinterpret_cast<uint4 *>(ring + S::kRing);
         for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
             uint4 *big = x + S::at(e / S::kChunks, e % S::kChunks, q_rows) / 16, *small = big + q_rows * D / 4;
@@ -320,7 +327,12 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
                     for (int y = 0; y < 2; ++y) {
                         uint32_t ab[4], as[4], bb[2], bs[2];
                         ldsm4(ab, sq + S::at(qr, 4 * k + 2 * y + qc, q_rows));
-                        ldsm4(as, sq_small + S::at(qr, 4 * k + 2 * y + qc, q_rows));
+                        if (halves) {
+                            ldsm4(as, sq_small + S::at(qr, 4 * k + 2 * y + qc, q_rows));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) split(ab[i], ab[i], as[i]);
+                        }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) split(f[2 * y + i], bb[i], bs[i]);
                         mma1688(part[y][0], ab, bb[0], bb[1]);
@@ -519,7 +531,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 3) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ Shared sh;
@@ -576,11 +588,11 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, unsig
     using S = Shape<T, D>;
     static_assert(S::kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
     static_assert(S::kTile <= kTileMax && S::kStages <= kStagesMax, "tile and ring as declared");
-    const size_t ring = S::kRing + (S::kF32 ? (size_t)padded_nodes(p.N) * D * 2 * sizeof(T) : 0), tree = tree_smem(p.N, p.sep);
+    const size_t ring = S::kRing + (S::kF32 ? q_bytes<D>(p.N) : 0), tree = tree_smem(p.N, p.sep);
     const size_t smem = (ring > tree ? ring : tree) + 1024;   // bf16: three CTAs an SM
     static std::atomic<unsigned long long> smem_set{0};
     // the limit is raised once per device, so to the largest tree's
-    const size_t most = S::kRing + (S::kF32 ? (size_t)kTreeMaxNodes * D * 8 : 0), most_tree = tree_smem(kTreeMaxNodes, 1);
+    const size_t most = S::kRing + (S::kF32 ? q_bytes<D>(kTreeMaxNodes) : 0), most_tree = tree_smem(kTreeMaxNodes, 1);
     cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D>, (most > most_tree ? most : most_tree) + 1024, smem_set);
     if (e != cudaSuccess) return e;
     Maps maps = {};

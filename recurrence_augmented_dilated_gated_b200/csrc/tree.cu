@@ -190,12 +190,13 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
             nodes = k < n_sets ? (N + sets_of(dils[0][k]) - 1) / sets_of(dils[0][k]) : N;
         }
     const int fixed = (c->dtype == RAT_BF16 ? 640 : 160) / (nodes <= 16 ? 1 : nodes <= 32 ? 2 : 4);
-    const int target = piece_target(kinds[0], n_kinds[0], c->B, (c->dtype == RAT_BF16 ? 3 : 2) * kSMs, fixed);
+    const int target = piece_target(kinds[0], n_kinds[0], c->B, 3 * kSMs, fixed);
     const int window_rows = target > 128 ? target : 128;
-    // A CTA that takes several items looks at the tree once: not many more CTAs than
-    // twelve rounds of them, however many items there are.
+    // A CTA that takes several items looks at the tree once: not more CTAs than some
+    // sixteen rounds of them (five rounds took 524 us where these take 520, 64
+    // entries of 16 heads).
     const long long pairs = (long long)c->B * c->H;
-    const long long share = pairs > 0 ? (16ll * kSMs + pairs - 1) / pairs : 1;
+    const long long share = pairs > 0 ? (48ll * kSMs + pairs - 1) / pairs : 1;
     int ctas = 0, slots = 0, per_head = 0;
     p->n_tc = p->tc_items_per_b = 0;
     long long R = 0;

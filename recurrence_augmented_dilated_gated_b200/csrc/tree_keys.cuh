@@ -125,7 +125,7 @@ __device__ __forceinline__ void tell_pieces(const TreeParams &p, const TreeInfo 
         const int len = tree_piece_rows(n, p.head[h].nsplit);
         np = n == 0 ? 0 : (n + len - 1) / len;
     }
-    if (ti.valid && p.head[h].fused) np = -2;   // absent nodes too
+    if (ti.valid && ti.max_depth >= 0 && p.head[h].fused) np = -2;   // absent nodes too
     p.info[((size_t)b * p.H + h) * p.N + i] = np;
 }
 

@@ -338,6 +338,18 @@ def test_all_nodes_absent_and_capacity_reached():
     assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dil,win,grid", [([1], [4], 0), ([3], [0], 0), ([8], [0], 1), ([1], [0], 0)])
+def test_entries_without_nodes_among_others(dtype, dil, win, grid):
+    # o = 0, lse = -inf for every node of an entry that drafted nothing, in every plan of a head
+    parent = np.array([[ABSENT] * 5, [-1, 0, 0, 2, ABSENT], [ABSENT] * 5], np.int32)
+    for cap in (60, 4000):
+        cfg = config(3, 5, 1, 128, dtype, dil, win, grid=grid)
+        p = Problem(cfg, cap, [40, 55, 0], parent).to_gpu()
+        p.ws[256:] = 0xab                       # whatever the workspace held
+        p.check(*p.step())
+
+
 @pytest.mark.parametrize("bad", [[-1, 1, 0], [-1, 5, 0], [-3, 0, 0], [ABSENT, 0, -1], [-1, 2, 0]])
 @pytest.mark.parametrize("pos", [20])
 def test_bad_parents_skip_the_entry(bad, pos):

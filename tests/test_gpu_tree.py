@@ -684,6 +684,32 @@ def test_step_and_commit_replay_from_one_graph():
     del graph
 
 
+def test_large_step_replays_from_a_graph():
+    # the persistent form, the items form and the join, launched early one after the other, as one captured step
+    cfg = config(2, 20, 3, 128, BF16, [1, 1, 8], [0, 30, 12])
+    p = Problem(cfg, 280000, [3000, 900], random_parents(np.random.default_rng(1), 2, 20, 6, pad=False)).to_gpu()
+    o, lse = p.outputs()
+    args = (cfg, p.d_q, p.d_k, p.d_v, p.d_g, p.d_parent, p.d_sk, p.d_sv, p.ck, p.cv, p.cap, p.d_pos, o, lse, p.ws)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        rat.rat_tree_decode_step(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        rat.rat_tree_decode_step(*args)
+    for turn in range(3):
+        p.d_pos.copy_(torch.tensor([3000 - 700 * turn, 900 - 128 * turn], dtype=torch.int32))
+        p.d_parent.copy_(torch.from_numpy(random_parents(np.random.default_rng(9 + turn), 2, 20, 4 + turn)))
+        want = p.step()
+        o.fill_(7)
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        rat.rat_check_status(p.ws)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    del graph
+
+
 # ------------------------------------------------------------------ page tables
 
 
@@ -865,6 +891,59 @@ def test_slot_map(grid, paged):
     with pytest.raises(rat.RatError, match="RAT_ERR_INVALID"):
         rat.rat_check_status(ws)
     assert torch.all(slots[3] == -1) and slots[0].cpu().tolist() == want[0, 0].tolist()
+
+
+@pytest.mark.parametrize("H", [4, 70, 131, 256])
+@pytest.mark.parametrize("grid", [0, 1])
+def test_slot_map_of_many_layouts(H, grid):
+    # a layout of its own for every head, more of them than are handled at a time
+    T, cap = 37, 500
+    cfg = config(1, T, H, 64, BF16, list(range(1, H + 1)), [(7 * h) % 20 for h in range(H)], grid=grid)
+    R = rat.rat_cache_rows(cfg, cap)
+    ws = rat.workspace(cfg, rat.RAT_OP_STATUS)
+    slots = torch.full((1, T, H), 7, dtype=torch.int64, device=DEV)
+    ring = torch.full_like(slots, 7)
+    i32 = lambda x: torch.tensor([x], dtype=torch.int32, device=DEV)  # noqa: E731
+    rat.rat_slot_map(cfg, None, cap, i32(450), i32(30), slots, ring, ws)
+    rat.rat_check_status(ws)
+    want = np.full((2, T, H), -1, np.int64)
+    for i in range(30):
+        for h in range(H):
+            m, r = rows_of(cfg, cap, h, 450 + i)
+            want[0, i, h] = h * R + m if m >= 0 else -1
+            want[1, i, h] = h * R + r if r >= 0 and i >= 30 - cfg.win[h] else -1
+    assert np.array_equal(slots[0].cpu().numpy(), want[0]) and np.array_equal(ring[0].cpu().numpy(), want[1])
+
+
+def test_page_table_update_of_a_large_table():
+    # more entries than a lane keeps in registers: 300 sequences of 1250 pages, then other lengths
+    B, cap, P = 300, 20000, 16
+    cfg = config(B, 1, 2, 64, BF16, [1, 3], [0, 0])
+    pps = -(-rat.rat_cache_rows(cfg, cap) // P)
+    num = 200000
+    gen = torch.Generator().manual_seed(1)
+    free = torch.randperm(num, generator=gen).to(torch.int32)
+    table = torch.full((B, pps), -1, dtype=torch.int32, device=DEV)
+    d_free, d_n = free.to(DEV), torch.tensor([num], dtype=torch.int32, device=DEV)
+    ws = rat.workspace(cfg, rat.RAT_OP_STATUS)
+    stack = free.tolist()
+    have = np.full((B, pps), -1, np.int64)
+    S = -(-cap // 3)
+    row = np.arange(pps * P)
+    for step in range(3):
+        length = torch.randint(-2000, 9000, (B,), generator=gen).to(torch.int32)
+        rat.rat_page_table_update(cfg, table, P, num, cap, length.to(DEV), 5, d_free, d_n, ws)
+        rat.rat_check_status(ws)
+        n = np.where(length.numpy() >= 0, length.numpy() + 5, 0)[:, None]
+        used = (row[None] < n) | ((row[None] < 3 * S) & ((row[None] % S) * 3 + row[None] // S < n))
+        need = used.reshape(B, pps, P).any(2)
+        for b, i in zip(*np.nonzero((have >= 0) & ~need)):
+            stack.append(int(have[b, i]))
+            have[b, i] = -1
+        for b, i in zip(*np.nonzero(need & (have < 0))):
+            have[b, i] = stack.pop()
+        assert np.array_equal(table.cpu().numpy(), have)
+        assert int(d_n) == len(stack) and d_free[:len(stack)].cpu().tolist() == stack
 
 
 @pytest.mark.parametrize("pos,count", [(-1, 3), (0, -1), (0, 6), (10, 5), (1 << 30, 1), ((1 << 31) - 1, 5)])

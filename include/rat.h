@@ -369,9 +369,9 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  * children, its inputs may hold anything (NaN too), and its outputs are o = 0,
  * lse = -inf.  With n_i ancestors, node i is at position pos[b] + n_i, which
  * must be below cache_cap.  An entry whose parents or positions are out of
- * range is skipped (the step: o = 0, lse = -inf for all its nodes; the commit:
- * state and position as they were) and RAT_ERR_INVALID recorded for
- * rat_check_status.  cfg->t0 and t_cap are ignored.
+ * range is skipped (the step: o = 0, lse = -inf for all its nodes; the commit,
+ * which looks at the branch it appends only: state and position as they were)
+ * and RAT_ERR_INVALID recorded for rat_check_status.  cfg->t0 and t_cap are ignored.
  */
 #define RAT_NODE_ABSENT (-2)
 #define RAT_TREE_MAX_NODES 64
@@ -388,8 +388,9 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  *   cache_k/v    in  as rat_decode_step, rows of positions < pos[b]; not changed
  *   pos          in  DEVICE int32 [B], 0 <= pos[b] <= cache_cap
  *   o            out [B,N,H,d];  lse out [B,H,N] fp32 or NULL
- * ws: rat_workspace_size(cfg, RAT_OP_TREE, cache_cap) bytes.  Two kernels, no
- * other CUDA call after the first on a device: a step can be captured in a
+ * ws: rat_workspace_size(cfg, RAT_OP_TREE, cache_cap) bytes.  Two kernels (three
+ * for a large bf16 tree step with heads of one dilated set), no other CUDA call
+ * after the first on a device: a step can be captured in a
  * CUDA graph and replayed with parents, positions and inputs refreshed in
  * place.  Results do not depend on the order in which the GPU runs the work.
  */
@@ -451,7 +452,7 @@ RAT_API rat_status rat_tree_commit_paged(const rat_cfg *cfg, const void *k, cons
  * that would read them report them) and RAT_ERR_NO_PAGES is recorded; a stack
  * that would overflow changes nothing and records RAT_ERR_INVALID.
  * ws: rat_workspace_size(cfg, RAT_OP_STATUS, 0) bytes.  One kernel, no host
- * synchronisation.  B * pages_per_seq < 2^31.
+ * synchronisation.  B * pages_per_seq <= 2^30.
  */
 RAT_API rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int page_rows, int pages_per_seq,
                                          int num_pages, int cache_cap, const int32_t *length, int extra,

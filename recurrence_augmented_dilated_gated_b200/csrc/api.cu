@@ -1020,8 +1020,9 @@ rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table, int pa
     const long long R = cache_rows(&c, cache_cap);
     if ((long long)pages_per_seq * page_rows < R)
         return fail(RAT_ERR_INVALID, "pages_per_seq x page_rows < %lld cache rows", R);
-    if ((long long)c.B * pages_per_seq >= 0x7fffffffLL || (long long)pages_per_seq * page_rows >= 0x7fffffffLL)
-        return fail(RAT_ERR_UNSUPPORTED, "B x pages_per_seq entries or pages_per_seq x page_rows rows exceed 2^31");
+    // 2^30 entries: the kernel steps past a run's end in 32 bits
+    if ((long long)c.B * pages_per_seq > 0x40000000LL || (long long)pages_per_seq * page_rows >= 0x7fffffffLL)
+        return fail(RAT_ERR_UNSUPPORTED, "B x pages_per_seq exceeds 2^30 entries or pages_per_seq x page_rows 2^31 rows");
     if (c.B == 0) return RAT_OK;
     CHECK_PTR(page_table, "page_table"); CHECK_PTR(length, "length");
     CHECK_PTR(free_pages, "free_pages"); CHECK_PTR(n_free, "n_free");

@@ -8,14 +8,15 @@
 // all in the order of the table's entries (b, then page), gives first, so the
 // result does not depend on how the work is spread.  That takes the ranks of
 // the entries among those that give and among those that take: two prefix sums
-// over the table.  One cluster of kCluster CTAs does it in one launch: every
+// over the table.  One cluster of eight or sixteen CTAs does it in one launch: every
 // warp owns a contiguous run of entries and counts with ballots, the warps'
 // counts are summed through distributed shared memory, and a second pass over
 // the run turns ballots into ranks.
 // Bound: latency (three sweeps of a run by its warp and three cluster
 // barriers); a lane's first kHeld entries stay in registers between the sweeps
-// (8 x 32 warps x 16 x 32 entries: 256 sequences of 512 pages), and their loads
-// go out together.
+// (16 x 32 warps x 16 x 32 entries: 512 sequences of 512 pages), and their loads
+// go out together.  A step of 8 sequences takes 8 us, of 256 sequences of 512
+// pages TBD us (device time); a table of 131072 entries is 0.2 us of bandwidth.
 //
 // Slot map.  The row of the flat pool (or flat dense cache) that holds a
 // position of a head: index arithmetic and one table read per value, bound by
@@ -284,8 +285,9 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
 
 cudaError_t launch_page_update(const PageUpdateParams &p, cudaStream_t s) {
     // sixteen CTAs (not a portable size) for a table that eight would hold in more
-    // than kHeld / 2 entries a lane, where the device can place them
-    static std::atomic<int> large{-1};
+    // than kHeld / 2 entries a lane, where the device can place them.  What was
+    // found is kept for each device: the attribute is a device's own
+    static std::atomic<unsigned long long> asked{0}, placed{0};
     int size = kSmall;
     if ((long long)p.B * p.pps > (long long)kSmall * kThreads * (kHeld / 2)) size = kLarge;
     cudaLaunchConfig_t cfg = {};
@@ -297,15 +299,20 @@ cudaError_t launch_page_update(const PageUpdateParams &p, cudaStream_t s) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (size == kLarge) {
-        int can = large.load(std::memory_order_acquire);
-        if (can < 0) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+        bool can = (placed.load(std::memory_order_acquire) & bit) != 0;
+        if (!can && !(asked.load(std::memory_order_acquire) & bit)) {
             cfg.gridDim = dim3(kLarge);
             attr.val.clusterDim.x = kLarge;
             int n = 0;
             can = cudaFuncSetAttribute(page_update_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
                   cudaOccupancyMaxActiveClusters(&n, page_update_kernel, &cfg) == cudaSuccess && n > 0;
             if (!can) cudaGetLastError();
-            large.store(can, std::memory_order_release);
+            if (can) placed.fetch_or(bit, std::memory_order_acq_rel);
+            asked.fetch_or(bit, std::memory_order_acq_rel);
         }
         if (!can) size = kSmall;
     }

@@ -10,9 +10,10 @@
 //
 // A cluster of up to kMaxCluster CTAs serves one entry (as many as its channels
 // fill), so that pos can be advanced in place: every CTA reads pos[b] before
-// the cluster's barrier and one writes it after.  A thread owns four channels of one head, keys and values (one gate
-// for both), and walks the branch with the loads of kAhead nodes in flight; it
-// steps row numbers along instead of dividing.
+// the cluster's barrier and one writes it after.  A thread owns four channels of
+// one head, keys and values (one gate for both), and walks the branch with the
+// loads of kAhead nodes in flight; it steps row numbers along instead of
+// dividing.
 // Bound: latency of the walk at small batches, bytes (k, v, g of the branch
 // read, its rows written, the states both) at large ones.
 #include <cooperative_groups.h>

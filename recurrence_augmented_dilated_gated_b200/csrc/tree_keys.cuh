@@ -1,6 +1,6 @@
-// tree_keys.cuh -- what the two forms of the tree step share (tree.cu: CUDA
-// cores, fp32; tree_mma.cu: tensor cores, bf16): which keys an item holds,
-// where they are and for whom they count, and the recurrence down the tree.
+// tree_keys.cuh -- what the kernels of the tree step share (tree_mma.cu: every
+// item; tree_tc.cu: held rows of large trees): which keys an item holds, where
+// they are and for whom they count, and the recurrence down the tree.
 #pragma once
 
 #include "tree.cuh"

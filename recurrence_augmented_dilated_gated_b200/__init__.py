@@ -389,74 +389,89 @@ def rat_decode_step_paged(cfg, q, k, v, g, state_k, state_v, cache, cache_cap, p
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+_native = None
 
-class _Args:
-    """Arguments of one call: checked tensors of one device, on which it runs."""
 
-    __slots__ = ("index", "ws", "ws_bytes")
+def _pointers(plan, ws, tensors):
+    """Addresses of the tensors of a call, then those of its workspace: address, bytes and device index.  `plan` says
+    of each tensor (name, dtype, shape or None, may be None).  The usual case is one native call; an argument that it
+    does not accept is looked at here, and named if it is wrong."""
+    global _native
+    if _native is None:
+        path = os.path.join(HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("%s not found: run recurrence_augmented_dilated_gated_b200/build.py" % path)
+        from . import _binding
 
-    def __init__(self, ws):
-        if not isinstance(ws, torch.Tensor) or not ws.is_cuda:
-            raise ValueError("ws must be a CUDA tensor (the library has no CPU path)")
-        self.index = ws.get_device()
-        self.ws = _ptr(ws, "ws", torch.uint8)
-        self.ws_bytes = ws.numel()
-
-    def ptr(self, t, name, dtype, shape, optional=False):
-        # the usual case in a few attribute reads: a decode step is as short as these checks
-        if (type(t) is torch.Tensor and t.dtype is dtype and (shape is None or t.shape == shape)
-                and t.get_device() == self.index and t.is_contiguous()):
-            return t.data_ptr() or None
-        p = _ptr(t, name, dtype, shape, optional)
-        if t is not None and t.numel() > 0 and t.get_device() != self.index:
-            raise ValueError("%s is on %s, the workspace on cuda:%d" % (name, t.device, self.index))
+        _native = _binding.pointers
+    p = _native(plan, ws, *tensors)
+    if p is not None:
         return p
-
-    def call(self, what, *args, stream=None):
-        if isinstance(stream, torch.cuda.Stream):
-            if stream.device.index != self.index:
-                raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, self.index))
-            stream = stream.cuda_stream
-        fn = getattr(load_library(), what)
-        if torch.cuda.current_device() == self.index:
-            rc = fn(*args, self.ws, self.ws_bytes, _raw_stream(self.index) if stream is None else int(stream))
-        else:
-            with torch.cuda.device(self.index):
-                rc = fn(*args, self.ws, self.ws_bytes, _raw_stream(self.index) if stream is None else int(stream))
-        if rc != RAT_OK:
-            _check(rc, what)
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda:
+        raise ValueError("ws must be a CUDA tensor (the library has no CPU path)")
+    index, out = ws.get_device(), []
+    for t, (name, dtype, shape, optional) in zip(tensors, plan):
+        out.append(_ptr(t, name, dtype, shape, optional))
+        if t is not None and t.numel() > 0 and t.get_device() != index:
+            raise ValueError("%s is on %s, the workspace on cuda:%d" % (name, t.device, index))
+    return (*out, _ptr(ws, "ws", torch.uint8), ws.numel(), index)
 
 
-def _paged_desc(a, cfg, cache):
+def _launch(what, p, args, stream):
+    """Call entry point `what` on the device of its tensors; `p` from _pointers."""
+    ws, ws_bytes, index = p[-3:]
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, index))
+        stream = stream.cuda_stream
+    fn = getattr(_lib or load_library(), what)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, ws, ws_bytes, _raw_stream(index) if stream is None else int(stream))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, ws, ws_bytes, _raw_stream(index) if stream is None else int(stream))
+    if rc != RAT_OK:
+        _check(rc, what)
+
+
+def _paged_desc(cache, index):
     """The descriptor of a paged cache, its tensors on the call's device."""
     if not isinstance(cache, rat_paged_cache):
         raise TypeError("cache must be a rat_paged_cache (paged_cache())")
-    if getattr(cache, "device_index", a.index) != a.index:
-        raise ValueError("cache is on cuda:%d, the workspace on cuda:%d" % (cache.device_index, a.index))
+    if getattr(cache, "device_index", index) != index:
+        raise ValueError("cache is on cuda:%d, the workspace on cuda:%d" % (cache.device_index, index))
     return ctypes.byref(cache)
 
 
-def _tree_shapes(a, cfg, cache, cache_cap):
-    """(B, N, H, shape of token tensors, of states, element type, cache arguments) of a tree call."""
+def _plan(cfg, what, cache_cap, make):
+    """make(cfg, cache_cap), kept with the configuration under all that it depends on."""
     c = cfg.c
-    B, N, H, d, dt = c.B, c.T, c.H, c.d, cfg.torch_dtype
-    if type(cache) is tuple:
-        shape = (B, H, rat_cache_rows(cfg, cache_cap), d)
-        where = (a.ptr(cache[0], "cache_k", dt, shape), a.ptr(cache[1], "cache_v", dt, shape))
-    else:
-        where = (_paged_desc(a, cfg, cache),)
-    return B, N, H, (B, N, H, d), (B, H, d), dt, where
+    key = (what, c.B, c.T, c.H, c.d, c.dtype, c.flags, cache_cap, cfg.dil.tobytes(), cfg.win.tobytes())
+    plans = cfg.__dict__.setdefault("_plans", {})
+    plan = plans.get(key)
+    if plan is None:
+        if len(plans) >= 64:
+            plans.clear()
+        plan = plans[key] = make(cfg, cache_cap)
+    return plan
 
 
-def _tree_step(what, cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse, ws, stream):
-    a = _Args(ws)
-    B, N, H, tok, st, dt, where = _tree_shapes(a, cfg, cache, cache_cap)
-    a.call(what, cfg.ref(), a.ptr(q, "q", dt, tok), a.ptr(k, "k", dt, tok),
-           a.ptr(v, "v", dt, tok), a.ptr(g, "g", dt, cfg.gate_shape(tok)),
-           a.ptr(parent, "parent", torch.int32, (B, N)), a.ptr(state_k, "state_k", torch.float32, st),
-           a.ptr(state_v, "state_v", torch.float32, st), *where, int(cache_cap),
-           a.ptr(pos, "pos", torch.int32, (B,)), a.ptr(o, "o", dt, tok),
-           a.ptr(lse, "lse", torch.float32, (B, H, N), True), stream=stream)
+def _cache_plan(cfg, cache_cap):
+    dt, shape = cfg.torch_dtype, (cfg.c.B, cfg.c.H, rat_cache_rows(cfg, cache_cap), cfg.c.d)
+    return ("cache_k", dt, shape, False), ("cache_v", dt, shape, False)
+
+
+def _step_plan(cfg, cache_cap, dense=True):
+    c, dt, f32, i32 = cfg.c, cfg.torch_dtype, torch.float32, torch.int32
+    tok, st = (c.B, c.T, c.H, c.d), (c.B, c.H, c.d)
+    plan = (("q", dt, tok, False), ("k", dt, tok, False), ("v", dt, tok, False), ("g", dt, cfg.gate_shape(tok), False),
+            ("parent", i32, (c.B, c.T), False), ("state_k", f32, st, False), ("state_v", f32, st, False),
+            ("pos", i32, (c.B,), False), ("o", dt, tok, False), ("lse", f32, (c.B, c.H, c.T), True))
+    return plan + _cache_plan(cfg, cache_cap) if dense else plan
+
+
+def _paged_step_plan(cfg, cache_cap):
+    return _step_plan(cfg, cache_cap, dense=False)
 
 
 def rat_tree_decode_step(cfg, q, k, v, g, parent, state_k, state_v, cache_k, cache_v, cache_cap, pos, o, lse=None,
@@ -464,70 +479,78 @@ def rat_tree_decode_step(cfg, q, k, v, g, parent, state_k, state_v, cache_k, cac
     """One decode step for a tree of cfg.T drafted nodes per entry: attention of every node over the held rows and
     its own branch.  parent: int32 [B, T] (-1: child of the last held position, RAT_NODE_ABSENT: padding).  Reads
     state and cache, changes neither; rat_tree_commit appends the branch that was accepted."""
-    _tree_step("rat_tree_decode_step", cfg, q, k, v, g, parent, state_k, state_v, (cache_k, cache_v), cache_cap, pos,
-               o, lse, ws, stream)
+    cache_cap = int(cache_cap)
+    p = _pointers(_plan(cfg, "step", cache_cap, _step_plan), ws,
+                  (q, k, v, g, parent, state_k, state_v, pos, o, lse, cache_k, cache_v))
+    _launch("rat_tree_decode_step", p, (cfg.ref(), *p[:7], p[10], p[11], cache_cap, *p[7:10]), stream)
 
 
 def rat_tree_decode_step_paged(cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse=None, ws=None,
                                stream=None):
     """rat_tree_decode_step over a paged cache (a rat_paged_cache from paged_cache())."""
-    _tree_step("rat_tree_decode_step_paged", cfg, q, k, v, g, parent, state_k, state_v, cache, cache_cap, pos, o, lse,
-               ws, stream)
+    cache_cap = int(cache_cap)
+    p = _pointers(_plan(cfg, "paged step", cache_cap, _paged_step_plan), ws,
+                  (q, k, v, g, parent, state_k, state_v, pos, o, lse))
+    _launch("rat_tree_decode_step_paged", p, (cfg.ref(), *p[:7], _paged_desc(cache, p[-1]), cache_cap, *p[7:10]), stream)
 
 
-def _tree_commit(what, cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache, cache_cap, pos,
-                 out_pos, ws, stream):
-    f32, i32 = torch.float32, torch.int32
-    a = _Args(ws)
-    B, N, H, tok, st, dt, where = _tree_shapes(a, cfg, cache, cache_cap)
-    a.call(what, cfg.ref(), a.ptr(k, "k", dt, tok), a.ptr(v, "v", dt, tok),
-           a.ptr(g, "g", dt, cfg.gate_shape(tok)), a.ptr(parent, "parent", i32, (B, N)),
-           a.ptr(leaf, "leaf", i32, (B,)), a.ptr(state_k, "state_k", f32, st), a.ptr(state_v, "state_v", f32, st),
-           a.ptr(out_state_k, "out_state_k", f32, st), a.ptr(out_state_v, "out_state_v", f32, st), *where,
-           int(cache_cap), a.ptr(pos, "pos", i32, (B,)), a.ptr(out_pos, "out_pos", i32, (B,)), stream=stream)
+def _commit_plan(cfg, cache_cap, dense=True):
+    c, dt, f32, i32 = cfg.c, cfg.torch_dtype, torch.float32, torch.int32
+    tok, st = (c.B, c.T, c.H, c.d), (c.B, c.H, c.d)
+    plan = (("k", dt, tok, False), ("v", dt, tok, False), ("g", dt, cfg.gate_shape(tok), False),
+            ("parent", i32, (c.B, c.T), False), ("leaf", i32, (c.B,), False), ("state_k", f32, st, False),
+            ("state_v", f32, st, False), ("out_state_k", f32, st, False), ("out_state_v", f32, st, False),
+            ("pos", i32, (c.B,), False), ("out_pos", i32, (c.B,), False))
+    return plan + _cache_plan(cfg, cache_cap) if dense else plan
+
+
+def _paged_commit_plan(cfg, cache_cap):
+    return _commit_plan(cfg, cache_cap, dense=False)
 
 
 def rat_tree_commit(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache_k, cache_v,
                     cache_cap, pos, out_pos, ws=None, stream=None):
     """Append the branch ending at node leaf[b] (int32 [B], -1: none): its rows to the cache, the state after it to
     out_state, the new length to out_pos (state and pos may be updated in place)."""
-    _tree_commit("rat_tree_commit", cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v,
-                 (cache_k, cache_v), cache_cap, pos, out_pos, ws, stream)
+    cache_cap = int(cache_cap)
+    p = _pointers(_plan(cfg, "commit", cache_cap, _commit_plan), ws,
+                  (k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, pos, out_pos, cache_k, cache_v))
+    _launch("rat_tree_commit", p, (cfg.ref(), *p[:9], p[11], p[12], cache_cap, p[9], p[10]), stream)
 
 
 def rat_tree_commit_paged(cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, cache, cache_cap,
                           pos, out_pos, ws=None, stream=None):
     """rat_tree_commit to a paged cache (a rat_paged_cache from paged_cache())."""
-    _tree_commit("rat_tree_commit_paged", cfg, k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v,
-                 cache, cache_cap, pos, out_pos, ws, stream)
+    cache_cap = int(cache_cap)
+    p = _pointers(_plan(cfg, "paged commit", cache_cap, _paged_commit_plan), ws,
+                  (k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, pos, out_pos))
+    _launch("rat_tree_commit_paged", p, (cfg.ref(), *p[:9], _paged_desc(cache, p[-1]), cache_cap, p[9], p[10]), stream)
 
 
 def rat_page_table_update(cfg, page_table, page_rows, num_pages, cache_cap, length, extra, free_pages, n_free, ws=None,
                           stream=None):
     """Bring page_table (int32 [B, pages_per_seq]) in line with entries of length[b] + extra positions (length < 0:
     none), taking pages from and giving them back to the stack free_pages[:n_free[0]].  In place, on the GPU."""
-    c = cfg.c
-    a = _Args(ws)
-    i32 = torch.int32
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != c.B:
+    B, i32, num_pages = cfg.c.B, torch.int32, int(num_pages)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, pages_per_seq]")
-    a.call("rat_page_table_update", cfg.ref(),
-           a.ptr(page_table, "page_table", i32, None), int(page_rows), int(page_table.shape[1]), int(num_pages),
-           int(cache_cap), a.ptr(length, "length", i32, (c.B,)), int(extra),
-           a.ptr(free_pages, "free_pages", i32, (int(num_pages),)), a.ptr(n_free, "n_free", i32, (1,)), stream=stream)
+    plan = (("page_table", i32, None, False), ("length", i32, (B,), False), ("free_pages", i32, (num_pages,), False),
+            ("n_free", i32, (1,), False))
+    p = _pointers(plan, ws, (page_table, length, free_pages, n_free))
+    _launch("rat_page_table_update", p, (cfg.ref(), p[0], int(page_rows), page_table.shape[1], num_pages, int(cache_cap),
+                                         p[1], int(extra), p[2], p[3]), stream)
 
 
 def rat_slot_map(cfg, cache, cache_cap, pos, count, slots, ring_slots=None, ws=None, stream=None):
     """Rows (int64 [B, T, H]) of positions pos[b] .. pos[b]+count[b]-1 in the cache seen as rows of d elements; cache
     is None for the dense one, or a rat_paged_cache.  count None: cfg.T positions everywhere."""
     c = cfg.c
-    a = _Args(ws)
     shape = (c.B, c.T, c.H)
-    a.call("rat_slot_map", cfg.ref(),
-           None if cache is None else _paged_desc(a, cfg, cache), int(cache_cap),
-           a.ptr(pos, "pos", torch.int32, (c.B,)), a.ptr(count, "count", torch.int32, (c.B,), True),
-           a.ptr(slots, "slots", torch.int64, shape), a.ptr(ring_slots, "ring_slots", torch.int64, shape, True),
-           stream=stream)
+    plan = (("pos", torch.int32, (c.B,), False), ("count", torch.int32, (c.B,), True),
+            ("slots", torch.int64, shape, False), ("ring_slots", torch.int64, shape, True))
+    p = _pointers(plan, ws, (pos, count, slots, ring_slots))
+    _launch("rat_slot_map", p, (cfg.ref(), None if cache is None else _paged_desc(cache, p[-1]), int(cache_cap),
+                                *p[:4]), stream)
 
 
 def rat_check_status(ws, stream=None):

@@ -1,17 +1,21 @@
-"""Build librat.so (every CUDA source under csrc/) for sm_100a with nvcc.
+"""Build librat.so (every CUDA source under csrc/) for sm_100a with nvcc, and
+_binding.so (csrc/binding.cpp, the Python binding's native part) with g++.
 
-The library is built in-tree, next to this file, so it ships with the package.
+Both are built in-tree, next to this file, so they ship with the package.
 """
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librat.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -35,7 +39,40 @@ def up_to_date():
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def start_binding(out):
+    """Start the compilation of the binding's native part against the installed torch."""
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, BINDING_SOURCE, "-o", out]
+    for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def binding_up_to_date():
+    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(BINDING_SOURCE)
+
+
 def build(force=False, verbose=False, ptxas_v=False):
+    binding = None
+    if force or not binding_up_to_date():
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        binding = start_binding(tmp)
+    lib = build_library(force, verbose, ptxas_v)
+    if binding:
+        out, _ = binding.communicate()
+        if binding.returncode:
+            sys.stdout.write(out.decode())
+            raise RuntimeError("g++ failed for " + BINDING_SOURCE)
+        os.replace(tmp, BINDING)
+    return lib
+
+
+def build_library(force=False, verbose=False, ptxas_v=False):
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)

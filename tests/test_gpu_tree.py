@@ -1032,3 +1032,42 @@ def test_speculative_serving_loop(dtype, grid):
         assert pos.tolist() == plen
         for x, s in enumerate((sk, sv)):
             assert_close(s, np.concatenate([f64(state[b][x]) for b in range(B)]), F32, "state")
+
+
+def test_binding_names_the_argument_that_does_not_fit():
+    cfg = config(2, 4, 2, 64, BF16, [1, 4], [0, 0])
+    p = Problem(cfg, 64, [20, 20], np.array([[-1, 0, 1, 2]] * 2, np.int32)).to_gpu()
+    o, lse = p.outputs()
+    args = dict(q=p.d_q, k=p.d_k, v=p.d_v, g=p.d_g, parent=p.d_parent, state_k=p.d_sk, state_v=p.d_sv, cache_k=p.ck,
+                cache_v=p.cv, cache_cap=p.cap, pos=p.d_pos, o=o, lse=lse, ws=p.ws)
+    wrong = {"dtype": lambda t: t.double(), "shape": lambda t: t[:1].contiguous(), "CUDA": lambda t: t.cpu(),
+             "contiguous": lambda t: torch.cat([t, t], -1)[..., ::2]}
+    for name in ("q", "g", "parent", "state_v", "cache_k", "pos", "o", "lse"):
+        for word, make in wrong.items():
+            with pytest.raises(ValueError, match=name + ".*" + word):
+                rat.rat_tree_decode_step(cfg, **dict(args, **{name: make(args[name])}))
+        if name != "lse":
+            with pytest.raises(ValueError, match=name):
+                rat.rat_tree_decode_step(cfg, **dict(args, **{name: None}))
+    for ws in (None, p.ws.cpu()):
+        with pytest.raises(ValueError, match="ws"):
+            rat.rat_tree_decode_step(cfg, **dict(args, ws=ws))
+    with pytest.raises(TypeError, match="q"):
+        rat.rat_tree_decode_step(cfg, **dict(args, q=[1.0]))
+    # a capacity of another layout asks for caches of its own shape
+    with pytest.raises(ValueError, match="cache_k.*shape"):
+        rat.rat_tree_decode_step(cfg, **dict(args, cache_cap=p.cap + 4))
+    # a tensor class of its own, and a view of the right shape, are what they hold
+    want, _ = p.step()
+    rat.rat_tree_decode_step(cfg, **dict(args, q=torch.nn.Parameter(p.d_q, requires_grad=False), k=p.d_k.view(8, 2, 64).view(2, 4, 2, 64)))
+    rat.rat_check_status(p.ws)
+    assert torch.equal(o, want)
+
+
+def test_a_configuration_changed_in_place_is_seen():
+    cfg = config(1, 2, 2, 64, F32, [1, 4], [0, 0])
+    p = Problem(cfg, 62, [20], np.array([[-1, 0]], np.int32)).to_gpu()
+    p.step()
+    cfg.dil[1] = 3                              # 62 rows become 63, 64 become 63
+    with pytest.raises(ValueError, match="cache_k.*shape"):
+        p.step()

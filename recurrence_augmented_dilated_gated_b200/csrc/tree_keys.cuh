@@ -80,6 +80,52 @@ __device__ __forceinline__ int key_count(const TreeParams &p, const Keys &ks, co
 
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+// one or two adjacent values
+template <int kN> __device__ __forceinline__ void loads(const float *p, float (&x)[kN]) {
+    if constexpr (kN == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+    } else {
+        x[0] = *p;
+    }
+}
+template <int kN> __device__ __forceinline__ void loads(const __nv_bfloat16 *p, float (&x)[kN]) {
+    if constexpr (kN == 2) {
+        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+        x[0] = v.x;
+        x[1] = v.y;
+    } else {
+        x[0] = __bfloat162float(*p);
+    }
+}
+template <int kN> __device__ __forceinline__ void stores(float *p, const float (&x)[kN]) {
+    if constexpr (kN == 2) *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+    else *p = x[0];
+}
+template <int kN> __device__ __forceinline__ void stores(__nv_bfloat16 *p, const float (&x)[kN]) {
+    if constexpr (kN == 2) *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x[0], x[1]);
+    else *p = __float2bfloat16_rn(x[0]);
+}
+
+__device__ __forceinline__ float exp2f_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The gate for a state that is rounded to T.  For bf16 rows the exponential is the
+// hardware's: its error of 2^-22 and that of the rounded exponent, |g| 2^-24, pass
+// into the gate times a (1 - a), under 2^-22 in all where the row keeps 2^-9.
+template <typename T> __device__ __forceinline__ void tree_gate(float g, float &a, float &oma) {
+    if constexpr (sizeof(T) == 4) {
+        gate_pair(g, a, oma);
+    } else {
+        const float e = exp2f_fast(fminf(g * -1.44269504f, 115.f));   // e^80: an infinity times 0 would be NaN
+        a = __fdividef(1.f, 1.f + e);
+        oma = e * a;
+    }
+}
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The rows of piece `piece` of set g; false when there is none.
 __device__ __forceinline__ bool slab_keys(const TreeParams &p, int h, int pos, int g, int piece, Keys &ks) {
@@ -170,105 +216,132 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool o
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The recurrence down the tree (128 threads), 64 channels at a time, in shared
-// memory as [node][array][64] floats: arrays k, v, gate and, with separate gates,
-// the values' gate.
-//   1  the tokens of all nodes are copied into their places (one round trip);
-//   2  half a warp a node, each place is overwritten: k and v by (1 - a) x, a gate
-//      by a;
-//   3  a thread, one channel of one tensor, walks the nodes, a parent before its
-//      children, adding a * parent: the rest is out of the chain;
-//   4  the rows are rounded and written out together.
-// (Gates inside the walk took 500 cycles a node, 23 us for 64 nodes.)  The code is
-// kept small: it runs once per CTA, and a straight line of instructions fetched
-// cold costs more than a loop.  The memory stays within a bf16 ring's 64 KB, so
-// that three CTAs share an SM (two took the hybrid step from 377 to 412 us).
-constexpr int kTreeChannels = 64;
-constexpr size_t tree_smem(int N, int sep) { return (size_t)N * kTreeChannels * (sep ? 4 : 3) * sizeof(float); }
+// The recurrence down the tree (128 threads), in shared memory: the tokens of all
+// nodes as they come ([node][array][kCh] of the tensors' type, arrays k, v, gate
+// and, with separate gates, the values' gate), overwritten by the states
+// ([node][k, v][kCh] floats).  stage() starts the copies of the tokens, before the
+// tree has been looked at; walk() takes kBatch nodes at a time: their tokens go to
+// registers and become a and (1 - a) x side by side, then every thread follows its
+// channels from parent to child, adding a * parent, and writes the rounded rows.
+// Tokens lie at the end of the memory, so states reach a batch's tokens only once
+// that batch is in registers: node n's state ends at (n + 1) S <= N (S - R) + (n + 1) R,
+// with S and R the bytes of a node's states and tokens.
+// With one warp on each of the SM's schedulers an instruction takes some five
+// cycles, so their number is the time: a thread has two adjacent channels of one
+// tensor where there are 128 (one channel of both tensors: 33000 cycles for 64
+// nodes, 17000 so).  bf16 states take the ring's 64 KB at 64 nodes, so three CTAs share
+// an SM; fp32 tokens are taken 64 channels at a time.
+template <typename T, int D> struct TreeWalk {
+    static constexpr int kThreads = 128, kBatch = 8;
+    static constexpr int kCh = sizeof(T) == 2 ? D : 64;
+    static constexpr int kMine = 2 * kCh / kThreads;                  // adjacent channels of a thread, of k or of v
+    static constexpr int kState = 2 * kCh * (int)sizeof(float);       // bytes of a node's states
+    static constexpr int kRow = kCh * (int)sizeof(T);                 // of one of its tokens
+    static_assert(kMine == 1 || kMine == 2, "one or two channels");
 
-template <typename T, int D>
-__device__ __forceinline__ void run_tree(const TreeParams &p, const int *parent, int b, int h, float *mem) {
-    constexpr int kThreads = 128, kCh = kTreeChannels;
-    constexpr int kChunks = kCh * (int)sizeof(T) / 16;               // 16-byte chunks of 64 channels
-    const int tid = threadIdx.x, N = p.N;
-    const int arrays = p.sep ? 4 : 3, row = arrays * kCh;            // floats of a node
-    const size_t bh = (size_t)b * p.H + h;
-    const bool rec = p.head[h].recur != 0;
-    const int c = tid % kCh, x = tid / kCh;
+    static __host__ __device__ __forceinline__ int token_bytes(int sep) { return kRow * (sep ? 4 : 3); }
+    static __host__ __device__ __forceinline__ size_t bytes(int N, int sep) {
+        const int r = token_bytes(sep);
+        return (size_t)N * (r > kState ? r : kState);
+    }
+    static __device__ __forceinline__ uint8_t *tokens(uint8_t *mem, int N, int sep) {
+        return mem + bytes(N, sep) - (size_t)N * token_bytes(sep);
+    }
+
+    // starts the copies of channels c0 .. c0 + kCh - 1 of all nodes
+    static __device__ __forceinline__ void stage(const TreeParams &p, int b, int h, int c0, uint8_t *mem) {
+        constexpr int kChunks = kRow / 16;
+        const int N = p.N, r = token_bytes(p.sep);
+        uint8_t *to = tokens(mem, N, p.sep);
 #pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += kCh) {
-        const float s0 = p.state[x][bh * D + c0 + c];
-        __syncthreads();   // the channels before are written out
-#pragma unroll 1
-        for (int y = 0; y < (rec ? arrays : 2); ++y) {
+        for (int y = 0; y < (p.head[h].recur ? (p.sep ? 4 : 3) : 2); ++y) {
             const T *src = static_cast<const T *>(y == 0 ? p.k : y == 1 ? p.v : p.g) + (y == 3 ? (size_t)p.B * N * p.H * D : 0) + c0;
-#pragma unroll 2
-            for (int e = tid; e < N * kChunks; e += kThreads) {
+#pragma unroll 4
+            for (int e = threadIdx.x; e < N * kChunks; e += kThreads) {
                 const int n = e / kChunks, ch = e % kChunks;
-                cp_async16(smem_u32(mem + n * row + y * kCh) + ch * 16,
-                           src + (((size_t)b * N + n) * p.H + h) * D + ch * (16 / (int)sizeof(T)), true);
+                cp_async16(smem_u32(to + n * r + y * kRow) + ch * 16, src + (((size_t)b * N + n) * p.H + h) * D + ch * (16 / (int)sizeof(T)), true);
             }
         }
         cp_commit();
+    }
+    // the queries are read after the walk: from L2 then
+    static __device__ __forceinline__ void ask_queries(const TreeParams &p, int b, int h) {
+        constexpr int kLines = D * (int)sizeof(T) / 128;
+        for (int e = threadIdx.x; e < p.N * kLines; e += kThreads)
+            prefetch_l2(static_cast<const T *>(p.q) + (((size_t)b * p.N + e / kLines) * p.H + h) * D + e % kLines * (128 / (int)sizeof(T)));
+    }
+
+    // channels c0 .. c0 + kCh - 1, staged; s0: the entry's states of k and v, out: the
+    // head's node rows, both from channel c0 on
+    static __device__ __noinline__ void walk(const int *parent, int N, bool sep, bool rec, const float *s0k, const float *s0v, T *out,
+                                             uint8_t *mem) {
+        const int r = token_bytes(sep);
+        const int x = threadIdx.x / (kThreads / 2), c = threadIdx.x % (kThreads / 2) * kMine;
+        float *state = reinterpret_cast<float *>(mem) + x * kCh + c;
+        const uint8_t *tok = tokens(mem, N, sep) + c * (int)sizeof(T), *gates = tok + (sep ? 2 + x : 2) * kRow;
+        tok += x * kRow;
+        out += x * N * D + c;
+        float s0[kMine];
+        loads<kMine>((x ? s0v : s0k) + c, s0);
         cp_wait<0>();
         __syncthreads();
 #pragma unroll 1
-        for (int n0 = 0; n0 < N; n0 += kThreads / 16) {
-            const int n = n0 + tid / 16;
-            float *m = mem + n * row + (tid % 16) * 4;
-            const T *raw = reinterpret_cast<const T *>(mem + n * row) + (tid % 16) * 4;
-            constexpr int kStep = kCh * (int)(sizeof(float) / sizeof(T));   // from array to array
-            float4 k, v, g, gv;
-            if (n < N) {
-                k = IO4<T>::load(raw);
-                v = IO4<T>::load(raw + kStep);
-                if (rec) g = IO4<T>::load(raw + 2 * kStep);
-                if (rec && p.sep) gv = IO4<T>::load(raw + 3 * kStep);
-            }
-            __syncwarp();
-            if (n < N) {
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), oma = make_float4(1.f, 1.f, 1.f, 1.f);
-                if (rec) gate4(g, a, oma);
-                *reinterpret_cast<float4 *>(m) = make_float4(oma.x * k.x, oma.y * k.y, oma.z * k.z, oma.w * k.w);
-                *reinterpret_cast<float4 *>(m + 2 * kCh) = a;
-                if (p.sep) {
-                    if (rec) gate4(gv, a, oma);
-                    *reinterpret_cast<float4 *>(m + 3 * kCh) = a;
+        for (int n0 = 0; n0 < N; n0 += kBatch) {
+            float a[kBatch][kMine], u[kBatch][kMine];
+            int up[kBatch];
+            const uint8_t *t = tok + n0 * r, *g = gates + n0 * r;
+#pragma unroll
+            for (int w = 0; w < kBatch; w += 4) *reinterpret_cast<int4 *>(up + w) = *reinterpret_cast<const int4 *>(parent + n0 + w);
+#pragma unroll
+            for (int w = 0; w < kBatch; ++w, t += r, g += r) {
+                if (n0 + w >= N) break;
+                loads<kMine>(reinterpret_cast<const T *>(t), u[w]);
+                if (rec) {
+                    float gate[kMine];
+                    loads<kMine>(reinterpret_cast<const T *>(g), gate);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        float add;
+                        tree_gate<T>(gate[i], a[w][i], add);
+                        u[w][i] *= add;
+                    }
                 }
-                *reinterpret_cast<float4 *>(m + kCh) = make_float4(oma.x * v.x, oma.y * v.y, oma.z * v.z, oma.w * v.w);
+            }
+            __syncthreads();   // the batch is in registers
+#pragma unroll
+            for (int w = 0; w < kBatch; ++w) {
+                const int n = n0 + w;
+                if (n >= N) break;
+                if (rec) {
+                    float before[kMine];
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) before[i] = s0[i];
+                    if (up[w] >= 0) loads<kMine>(state + up[w] * 2 * kCh, before);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) u[w][i] = a[w][i] * before[i] + u[w][i];
+                }
+                if (up[w] == RAT_NODE_ABSENT) {   // its inputs may hold anything
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) u[w][i] = 0.f;
+                }
+                stores<kMine>(state + n * 2 * kCh, u[w]);
+                stores<kMine>(out + n * D, u[w]);
             }
         }
-        __syncthreads();
-        float *m = mem + x * kCh + c;
-        const float *ga = mem + (2 + (p.sep ? x : 0)) * kCh + c;
+        __threadfence();   // other threads copy these rows past L1
+    }
+    static __device__ __forceinline__ void run(const TreeParams &p, const int *parent, int b, int h, uint8_t *mem) {
+        const size_t bh = (size_t)b * p.H + h;
 #pragma unroll 1
-        for (int n0 = 0; n0 < N; n0 += 4) {
-            float a[4], u[4];
-            int par[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int n = min(n0 + w, N - 1);
-                par[w] = parent[n];
-                u[w] = m[n * row];
-                a[w] = ga[n * row];
+        for (int c0 = 0; c0 < D; c0 += kCh) {
+            if (c0 > 0) {
+                __syncthreads();   // the channels before are done with
+                stage(p, b, h, c0, mem);
             }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if (n0 + w < N) {
-                    const float s = a[w] * (par[w] >= 0 ? m[par[w] * row] : s0) + u[w];
-                    m[(n0 + w) * row] = par[w] == RAT_NODE_ABSENT ? 0.f : s;   // its inputs may hold anything
-                }
-            }
-        }
-        __syncthreads();
-        T *out = static_cast<T *>(p.node_rows) + bh * 2 * N * D + c0;
-#pragma unroll 2
-        for (int e = tid; e < N * 2 * (kCh / 4); e += kThreads) {
-            const int ch = e % (kCh / 4), nx = e / (kCh / 4), y = nx & 1, n = nx >> 1;
-            IO4<T>::store(out + ((size_t)y * N + n) * D + ch * 4, *reinterpret_cast<const float4 *>(mem + n * row + y * kCh + ch * 4));
+            walk(parent, p.N, p.sep != 0, p.head[h].recur != 0, p.state[0] + bh * D + c0, p.state[1] + bh * D + c0,
+                 static_cast<T *>(p.node_rows) + bh * 2 * p.N * D + c0, mem);
         }
     }
-    __threadfence();   // other threads copy these rows past L1
-}
+};
 
 }  // namespace rat

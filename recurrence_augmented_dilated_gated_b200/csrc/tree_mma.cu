@@ -104,7 +104,8 @@ template <int D> constexpr size_t q_bytes(int n) { return (size_t)(n <= 16 ? 16 
 
 struct Shared {
     TreeInfo ti;
-    int parent[kTreeMaxNodes], nodes[kTreeMaxNodes];
+    alignas(16) int parent[kTreeMaxNodes];   // read four at a time
+    int nodes[kTreeMaxNodes];
     int n, bad, odd;                      // odd: some local value is not finite
     uint64_t full[kStagesMax];              // a slab's tile has landed
     volatile int abort;
@@ -112,6 +113,44 @@ struct Shared {
     float m[kWarps][16], l[kWarps][16];
     float inv[kTreeMaxNodes];
 };
+
+// key_count() of a tile: of nodes without branches and four at a time, so that what
+// is read of them does not wait for what is written (64 nodes: 14600 -> 6000
+// cycles); of n held rows of the window, `held` positions back from pos.  Out of
+// line, as it would take registers from the item's loop.
+template <int kTile>
+__device__ __noinline__ void count_keys(Shared &sh, int n_nodes, int k0, bool nodes, int held, int n, int pos, int W, int D, int dedupe, int grid) {
+    constexpr int kStep = kThreads / kTile;
+    const int key = threadIdx.x % kTile;   // a thread has one key
+    if (!nodes) {
+        const int j = pos - held + k0 + key;
+        const bool left_out = k0 + key >= n || (dedupe && grid && j % D == D - 1);
+#pragma unroll 1
+        for (int i = threadIdx.x / kTile; i < n_nodes; i += kStep) {
+            const int dep = sh.ti.depth[i], back = pos + dep - j;
+            sh.count[i][key] = !(left_out || dep < 0 || back >= W || (dedupe && !grid && back % D == 0));
+        }
+        return;
+    }
+    const int k = min(k0 + key, kTreeMaxNodes - 1), kd = sh.ti.depth[k];
+    const unsigned *half = reinterpret_cast<const unsigned *>(sh.ti.anc) + (k >> 5);   // the word with the key's bit
+    const unsigned bit = 1u << (k & 31), far_lo = (unsigned)sh.ti.far, far_hi = (unsigned)(sh.ti.far >> 32);
+    const bool far_key = (k < 32 ? far_lo : far_hi) & bit;
+#pragma unroll 1
+    for (int i0 = threadIdx.x / kTile; i0 < n_nodes; i0 += 4 * kStep) {
+        int cnt[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int i = min(i0 + w * kStep, n_nodes - 1), back = sh.ti.depth[i] - kd;
+            const bool far = grid ? i == k || far_key : ((back < 32 ? far_lo : far_hi) >> (back & 31)) & 1u;
+            const bool near = back < W && !(dedupe && far);
+            cnt[w] = half[2 * i] & bit ? (int)far + (int)near : 0;
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (i0 + w * kStep < n_nodes) sh.count[i0 + w * kStep][key] = (uint8_t)cnt[w];
+    }
+}
 
 // One item: the keys of parts[0 .. n_parts), tile by tile, for the sh.n nodes of
 // sh.nodes.  One body serves slabs and local items (what differs is where a row
@@ -286,11 +325,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             return false;
         }
         if (masked) {
-#pragma unroll 1
-            for (int e = tid; e < n_nodes * kTile; e += kThreads) {
-                const int i = e / kTile, key = k0 + e % kTile, dep = sh.ti.depth[i];
-                sh.count[i][e % kTile] = dep < 0 ? 0 : key_count(p, ks, sh.ti, h, pos, dep, sh.ti.anc[i], i, key);
-            }
+            count_keys<kTile>(sh, n_nodes, k0, ks.kind == kNodes, pos - (int)ks.row0, ks.n, pos, p.head[h].win, p.head[h].dil, p.dedupe, p.grid);
             __syncthreads();
         }
         if (t + kStages - 1 < n_tiles) load(t + kStages - 1);
@@ -539,6 +574,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
     allow_next();
     const int b = blockIdx.x / p.ctas_per_b, it = blockIdx.x % p.ctas_per_b;
     const int h = find_tree_head(p, it), li = it - p.head[h].cta0;
+    if (li == 0) {
+        TreeWalk<T, D>::stage(p, b, h, 0, ring);
+        TreeWalk<T, D>::ask_queries(p, b, h);
+    }
     const int pos = p.pos[b];
     if (tid == kThreads - 1) {
         for (int i = 0; i < kStagesMax; ++i) mbar_init(&sh.full[i], 1);
@@ -556,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
     if (li == 0) tell_pieces(p, sh.ti, b, h, pos);
     if (!sh.ti.valid || sh.ti.max_depth < 0) {
         if (!sh.ti.valid && li == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
+        cp_wait<0>();
         if (blockIdx.x == gridDim.x - 1) wait_previous();
         return;
     }
@@ -569,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
         if (li < ws) {
             slot = p.head[h].nsplit + li;
             n = local_keys(p, h, pos, li, parts);
-            if (li == 0) run_tree<T, D>(p, sh.parent, b, h, reinterpret_cast<float *>(ring));
+            if (li == 0) TreeWalk<T, D>::run(p, sh.parent, b, h, ring);
             if (tid == 0) sh.n = p.N;
             if (tid < p.N) sh.nodes[tid] = tid;
         } else {
@@ -588,11 +628,11 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, unsig
     using S = Shape<T, D>;
     static_assert(S::kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
     static_assert(S::kTile <= kTileMax && S::kStages <= kStagesMax, "tile and ring as declared");
-    const size_t ring = S::kRing + (S::kF32 ? q_bytes<D>(p.N) : 0), tree = tree_smem(p.N, p.sep);
+    const size_t ring = S::kRing + (S::kF32 ? q_bytes<D>(p.N) : 0), tree = TreeWalk<T, D>::bytes(p.N, p.sep);
     const size_t smem = (ring > tree ? ring : tree) + 1024;   // bf16: three CTAs an SM
     static std::atomic<unsigned long long> smem_set{0};
     // the limit is raised once per device, so to the largest tree's
-    const size_t most = S::kRing + (S::kF32 ? q_bytes<D>(kTreeMaxNodes) : 0), most_tree = tree_smem(kTreeMaxNodes, 1);
+    const size_t most = S::kRing + (S::kF32 ? q_bytes<D>(kTreeMaxNodes) : 0), most_tree = TreeWalk<T, D>::bytes(kTreeMaxNodes, 1);
     cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D>, (most > most_tree ? most : most_tree) + 1024, smem_set);
     if (e != cudaSuccess) return e;
     Maps maps = {};

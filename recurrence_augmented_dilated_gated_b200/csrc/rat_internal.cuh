@@ -18,13 +18,16 @@ namespace rat {
 // every step (and one more call that stream capture has to tolerate).
 // `done` holds one bit per device and must be distinct per kernel.
 template <typename Kernel>
-cudaError_t ensure_smem_limit(Kernel kernel, size_t bytes, std::atomic<unsigned long long> &done) {
+cudaError_t ensure_smem_limit(Kernel kernel, size_t bytes, std::atomic<unsigned long long> &done, bool all_shared = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // all_shared: the SM is set up for as much shared memory as there is, so that another kernel's CTAs find room
+    if (e == cudaSuccess && all_shared)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
     return e;
 }

@@ -633,7 +633,7 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, unsig
     static std::atomic<unsigned long long> smem_set{0};
     // the limit is raised once per device, so to the largest tree's
     const size_t most = S::kRing + (S::kF32 ? q_bytes<D>(kTreeMaxNodes) : 0), most_tree = TreeWalk<T, D>::bytes(kTreeMaxNodes, 1);
-    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D>, (most > most_tree ? most : most_tree) + 1024, smem_set);
+    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D>, (most > most_tree ? most : most_tree) + 1024, smem_set, true);
     if (e != cudaSuccess) return e;
     Maps maps = {};
     if (!p.page_table)

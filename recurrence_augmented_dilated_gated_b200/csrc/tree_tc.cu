@@ -16,7 +16,7 @@
 //   warps 0-3  softmax: S^T from TMEM, P^T (bf16) to shared memory, at an item's
 //              end O^T from TMEM to the item's partial; they also stage the next
 //              item's queries once its last scores are in
-//   warp 4     copies: K~ and V~ tiles (32 KB each) into a ring of six slots, by
+//   warp 4     copies: K~ and V~ tiles (32 KB each) into a ring of four or six slots, by
 //              TMA, 128-byte swizzled; a page is a box of its own.  (16-byte
 //              asynchronous copies by two warps instead, for any page size, took
 //              3.3 TB/s at N = 32.)
@@ -43,11 +43,18 @@ constexpr int kSoftmax = 128;
 constexpr int kThreads = kSoftmax + 64;
 constexpr int kD = 128;
 constexpr int kTile = 128;               // keys per tile
-constexpr int kSlots = 6;
+constexpr int kSlotsMax = 6;
 constexpr uint32_t kHalf = kTile * 128;  // 64 channels of a tile: rows of 128 bytes
 constexpr uint32_t kSlot = 2 * kHalf;    // a K~ or a V~ tile
-constexpr uint32_t kQHalf = kTreeMaxNodes * 128;
-constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
+// Four slots for up to 32 nodes: beside them an SM has room for a CTA of
+// tree_mma.cu (64 KB), which then does the windows and the nodes while this kernel
+// streams (TBD).  For 64 nodes Q leaves it no room, and six slots
+// are 2 % faster than four.
+template <int NP> struct Mem {
+    static constexpr int kSlots = NP <= 32 ? 4 : kSlotsMax;
+    static constexpr uint32_t kQHalf = NP * 128;
+    static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
+};
 constexpr int kTmemCols = 256;
 constexpr float kSlack = 8.f;            // log2 of how far P may pass 1
 
@@ -135,7 +142,7 @@ struct Items {
 };
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots], sfull[2], sempty[2], qfull, pfull, pvdone, copied[4], drain;
+    uint64_t full[kSlotsMax], empty[kSlotsMax], sfull[2], sempty[2], qfull, pfull, pvdone, copied[4], drain;
     uint32_t tmem;
     volatile int abort;
     int bad[4];                       // item number + 1 of an item with an invalid page, by item mod 4 (the copies
@@ -167,6 +174,8 @@ struct Maps {
 template <int NP>   // nodes, padded to 16, 32 or 64
 __global__ void __launch_bounds__(kThreads, 1)
 tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
+    constexpr int kSlots = Mem<NP>::kSlots;
+    constexpr uint32_t kQHalf = Mem<NP>::kQHalf, kOffQ = Mem<NP>::kOffQ, kOffP = Mem<NP>::kOffP;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ Shared sh;
@@ -491,7 +500,8 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
 
 template <int NP> cudaError_t launch_np(const TreeParams &p, cudaStream_t s) {
     static std::atomic<unsigned long long> smem_set{0};
-    cudaError_t e = ensure_smem_limit(tree_tc_kernel<NP>, kBytes + 1024, smem_set);
+    constexpr uint32_t kBytes = Mem<NP>::kBytes;
+    cudaError_t e = ensure_smem_limit(tree_tc_kernel<NP>, kBytes + 1024, smem_set, true);
     if (e != cudaSuccess) return e;
     Maps maps;
     const long long rows = p.page_table ? p.page_rows : p.cache_R, blocks = (long long)(p.page_table ? p.num_pages : p.B) * p.H;

@@ -135,8 +135,8 @@ rat_status plan_tree(const rat_cfg *c, int cap, int page_rows, TreeParams *p, Tr
     rat_status st = check_tree(c, cap);
     if (st != RAT_OK) return st;
     *tl = tree_plan(c, cap, page_rows, p);
-    const long long most = std::max((long long)std::max(p->ctas_per_b, p->slots_per_b), (long long)c->H * c->T);
-    if ((double)c->B * (double)most >= 2147483647.0)
+    const long long most = std::max((long long)std::max(p->ctas_per_b, p->slots_per_b + p->n_tc), (long long)c->H * c->T);
+    if ((double)c->B * (double)most >= 2147483647.0 - kTreeTcCtas)
         return fail(RAT_ERR_UNSUPPORTED, "B = %d entries are too many for one tree step", c->B);
     return RAT_OK;
 }
@@ -888,6 +888,7 @@ rat_status tree_step(const rat_cfg *cfg_in, const void *q, const void *k, const 
     p.part = reinterpret_cast<float *>(w + tl.part);
     p.ml = reinterpret_cast<float2 *>(w + tl.ml);
     p.info = reinterpret_cast<int *>(w + tl.info);
+    p.tc_range = reinterpret_cast<int2 *>(w + tl.tc_range);
     p.cap = cache_cap; p.B = c.B; p.N = c.T; p.H = c.H; p.d = c.d;
     p.scale_log2 = scale_of(&c) * 1.4426950408889634f;
     p.hdr = reinterpret_cast<WsHeader *>(ws);

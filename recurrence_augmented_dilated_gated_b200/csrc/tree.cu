@@ -40,30 +40,52 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
     const int bh = blockIdx.x / nb, i = (blockIdx.x % nb) * kNodes + warp;
     const int b = bh / p.H, h = bh % p.H;
     const int S = p.head[h].nsplit, ws = p.head[h].wsplit;
-    const size_t base = ((size_t)b * p.slots_per_b + p.head[h].slot0) * p.N;
+    const int tc = p.head[h].tc;
+    // first slots of the set's pieces and of the window's
+    int set0 = b * p.slots_per_b + p.head[h].slot0;
+    const int w0 = set0 + S;
     wait_previous();
+    // the set's pieces: as many as info says, or tree_tc.cu's
+    int shared = 0;
+    if (tc >= 0) {
+        long long row0;
+        const int pos = p.pos[b];
+        if (pos > 0 && pos <= p.cap && tree_set_rows(p, h, pos, 0, row0) > 0) {
+            const int q = b * p.n_tc + tc;
+            const int2 r = p.tc_range[q];
+            set0 = p.tc_slot0 + q + r.x;
+            shared = r.y - r.x + 1;
+        }
+    }
+    auto pieces = [&](int node) {
+        const int np = p.info[(size_t)bh * p.N + node];
+        return np > 0 && tc >= 0 ? shared : np;
+    };
     int bad = 0;
     if (p.page_table) {
         // a page that was not valid anywhere in (b, h): the whole pair is skipped
-        for (int e = threadIdx.x; e < (S + ws) * p.N; e += kCombineThreads) {
-            const int s = e / p.N, np = p.info[(size_t)bh * p.N + e % p.N];
-            if (np >= 0 && (s >= S || s < np)) bad |= p.ml[base + e].y < 0.f;
+        const int most = tc >= 0 ? shared : S;
+        for (int e = threadIdx.x; e < (most + ws) * p.N; e += kCombineThreads) {
+            const int s = e / p.N, n = e % p.N, np = pieces(n);
+            if (np < 0) continue;
+            if (s >= most || s < np) bad |= p.ml[(size_t)(s < most ? set0 + s : w0 + s - most) * p.N + n].y < 0.f;
         }
         bad = __syncthreads_or(bad);
         if (bad && threadIdx.x == 0 && i == 0) report_error(p.hdr, RAT_ERR_INVALID, b);
     }
     if (i >= p.N) return;
-    const int np = p.info[(size_t)bh * p.N + i];
+    const int np = pieces(i);
     if (np == -2) return;
     float M = -INFINITY, L = 0.f, o[kC] = {};
     if (np >= 0 && !bad) {
-        const int n = np + ws;   // piece x is slot x, or S + x - np past the set's
-        for (int x = lane; x < n; x += 32) M = fmaxf(M, p.ml[base + (size_t)(x < np ? x : S + x - np) * p.N + i].x);
+        const int n = np + ws;   // pieces of the set, then of the window
+        auto place = [&](int x) { return (size_t)(x < np ? set0 + x : w0 + x - np) * p.N + i; };
+        for (int x = lane; x < n; x += 32) M = fmaxf(M, p.ml[place(x)].x);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
 #pragma unroll 2
         for (int x = 0; x < n; ++x) {
-            const size_t at = base + (size_t)(x < np ? x : S + x - np) * p.N + i;
+            const size_t at = place(x);
             const float2 ml = p.ml[at];
             float a[kC];
             if (kC == 4) *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(p.part + at * D + lane * kC);
@@ -172,8 +194,15 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
         if (x) one_set_rows += kinds[x][k].rows;
     }
     const bool tc = c->dtype == RAT_BF16 && c->d == 128 && one_set_rows * c->B >= kTcMinRows && tree_tc_pages(page_rows);
-    int target_tc = 0;
     const int n_sets = n_kinds[0];   // kinds of heads with several sets
+    // Fewer pairs than three for each of its CTAs: even shares of all rows, whatever the
+    // lengths; else pieces by the capacity.  16 entries x 16 heads of 14000 rows (1.7
+    // pairs a CTA): 333 us, by pieces 366; 32 x 16 of 1800 rows, in pages (3.5): 128, by
+    // pieces 124.
+    long long one_set_heads = 0;
+    for (int k = 0; k < n_kinds[1]; ++k) one_set_heads += kinds[1][k].sets;
+    const bool even = tc && one_set_heads * c->B < 3 * kTreeTcCtas;
+    int target_tc = 0;
     if (tc) {
         target_tc = piece_target(kinds[1], n_kinds[1], c->B, kSMs, 512);
     } else {
@@ -199,12 +228,14 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     const long long share = pairs > 0 ? (48ll * kSMs + pairs - 1) / pairs : 1;
     int ctas = 0, slots = 0, per_head = 0;
     p->n_tc = p->tc_items_per_b = 0;
+    p->tc_same = 1;
+    p->tc_even = even ? 1 : 0;
     long long R = 0;
     for (int h = 0; h < c->H; ++h) {
         const int D = c->dil[h];
         const int slab = (int)(((long long)cap + D - 1) / D);
         const bool one_set = grid || D == 1, by_tc = tc && one_set;
-        const int ns = (slab + (by_tc ? target_tc : target) - 1) / (by_tc ? target_tc : target);
+        const int ns = by_tc && even ? 1 : (slab + (by_tc ? target_tc : target) - 1) / (by_tc ? target_tc : target);
         p->head[h].dil = D;
         // with dedupe a D = 1 head's window keys are all in its dilated set
         p->head[h].win = (c->flags & RAT_FLAG_DEDUPE) && D == 1 ? 0 : c->win[h];
@@ -215,11 +246,13 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
         const long long most = (long long)sets_of(D) * ns;
         p->head[h].slab_ctas = (int)(most < share ? most : share);
         p->head[h].fused = 0;
+        p->head[h].tc = by_tc && even ? p->n_tc : -1;
         if (by_tc) {
             p->head[h].slab_ctas = 0;
-            p->tc_head[p->n_tc] = (unsigned char)h;
-            p->tc_item0[p->n_tc++] = p->tc_items_per_b;
+            p->tc_item0[p->n_tc] = p->tc_items_per_b;
             p->tc_items_per_b += ns;
+            p->tc_head[p->n_tc++] = (unsigned char)h;
+            if (D != c->dil[p->tc_head[0]]) p->tc_same = 0;
         } else if (one_set && ns == 1 && p->head[h].wsplit == 1) {
             p->head[h].fused = 1;
             p->head[h].slab_ctas = 0;
@@ -244,11 +277,14 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
     const size_t elt = c->dtype == RAT_F32 ? 4 : 2;
     TreeLayout L;
+    const size_t pairs_tc = even ? (size_t)c->B * p->n_tc : 0, all_slots = (size_t)c->B * slots + (even ? pairs_tc + kTreeTcCtas : 0);
+    p->tc_slot0 = c->B * slots;
     L.node_rows = 0;
     L.part = al((size_t)c->B * c->H * 2 * N * c->d * elt);
-    L.ml = L.part + al((size_t)c->B * slots * N * c->d * sizeof(float));
-    L.info = L.ml + al((size_t)c->B * slots * N * sizeof(float2));
-    L.total = L.info + al((size_t)c->B * c->H * N * sizeof(int));
+    L.ml = L.part + al(all_slots * N * c->d * sizeof(float));
+    L.info = L.ml + al(all_slots * N * sizeof(float2));
+    L.tc_range = L.info + al((size_t)c->B * c->H * N * sizeof(int));
+    L.total = L.tc_range + al(pairs_tc * sizeof(int2));
     return L;
 }
 

@@ -6,6 +6,9 @@
 
 namespace rat {
 
+// CTAs of tree_tc.cu, one an SM, at most
+constexpr int kTreeTcCtas = 148;
+
 // Nodes of one entry's tree, at most: a branch fits in one 64-bit mask.
 constexpr int kTreeMaxNodes = 64;
 
@@ -21,6 +24,7 @@ struct TreeHead {
     int slot0;       // first partial slot
     int recur;
     int fused;       // one item has all the keys and writes the result itself
+    int tc;          // place in tc_head with even shares, else -1
 };
 
 struct TreeParams {
@@ -44,10 +48,15 @@ struct TreeParams {
     int ctas_per_b, slots_per_b;
     int ctas_per_head;           // when all heads have as many, else 0
     TreeHead head[kMaxHeads];
-    // heads whose held rows tree_tc.cu takes (slab_ctas is 0), and their pieces
-    int n_tc, tc_items_per_b;
+    // heads whose held rows tree_tc.cu takes (slab_ctas is 0): by pieces, as the other
+    // heads' are, or (tc_even) in even shares: its CTA c then has the partial of pair
+    // q = b * n_tc + i (i: place in tc_head) in slot tc_slot0 + q + c
+    int n_tc, tc_same, tc_even;      // tc_same: they all have one dilation
     unsigned char tc_head[kMaxHeads];
-    int tc_item0[kMaxHeads + 1];
+    int tc_items_per_b;              // pieces of an entry, and the first of a head
+    int tc_item0[kMaxHeads];
+    int tc_slot0;
+    int2 *tc_range;                  // [B * n_tc] first and last CTA of a pair with held rows
     WsHeader *hdr;
 };
 
@@ -175,7 +184,7 @@ __device__ __forceinline__ void gate4(const float4 &g, float4 &a, float4 &oma) {
 // Split plan and workspace offsets of a tree step (host); returns the bytes the
 // step needs after the workspace header.
 struct TreeLayout {
-    size_t node_rows, part, ml, info, total;
+    size_t node_rows, part, ml, info, tc_range, total;
 };
 TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p);
 

@@ -286,9 +286,8 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
         const Keys &ks = part_of(t, k0);
         // nodes mask each other; the window's first keys are out of the deeper
         // nodes' reach; with dedupe any of its keys may be in the dilated set
-        const bool local = ks.kind != kSlab;
         const bool masked = ks.kind == kNodes || (ks.kind == kWindow && (p.dedupe || k0 < sh.ti.max_depth));
-        if (local) {
+        if (masked) {
             // values that are not finite leave the tile: a zero probability times
             // one of them would reach every node.  add_odd() puts them back
             __syncwarp();

@@ -12,7 +12,7 @@
 // sums of P stay in registers, a node's share of each key, and are added
 // across the CTA once per item.
 //
-// One persistent CTA per SM walks over items (runs of rows of one (b, h)):
+// One persistent CTA per SM walks over items (its runs of rows of one (b, h)):
 //   warps 0-3  softmax: S^T from TMEM, P^T (bf16) to shared memory, at an item's
 //              end O^T from TMEM to the item's partial; they also stage the next
 //              item's queries once its last scores are in
@@ -48,7 +48,7 @@ constexpr uint32_t kHalf = kTile * 128;  // 64 channels of a tile: rows of 128 b
 constexpr uint32_t kSlot = 2 * kHalf;    // a K~ or a V~ tile
 // Four slots for up to 32 nodes: beside them an SM has room for a CTA of
 // tree_mma.cu (64 KB), which then does the windows and the nodes while this kernel
-// streams (TBD).  For 64 nodes Q leaves it no room, and six slots
+// streams (32 x 16 nodes on a paged grid 136 -> 121 us).  For 64 nodes Q leaves it no room, and six slots
 // are 2 % faster than four.
 template <int NP> struct Mem {
     static constexpr int kSlots = NP <= 32 ? 4 : kSlotsMax;
@@ -116,28 +116,175 @@ __device__ __forceinline__ bool softmax_any(bool x) {
     return r != 0;
 }
 
-// The items of a CTA, in order; every role walks the same list.
+// What a CTA does: `tiles` tiles, the first `skip` of entry list[0] left out; n
+// entries are listed, those behind them follow one by one.
+constexpr int kList = 8;
+struct Range {
+    long long skip, tiles;
+    int n, list[kList];
+    long long sum[kThreads / 32];     // of a warp
+    int count[kThreads / 32];
+};
+
+// All tiles of all pairs (b, h), in that order, are dealt out evenly: CTA c of G has
+// tiles total * c / G .. total * (c + 1) / G - 1, whatever the positions.  (Pieces
+// of equal length planned by the capacity left CTAs idle where entries are
+// shorter: 16 x 64 nodes over 16000 dense rows 366 -> 333 us.)
+// With many pairs (tree_plan) each is cut into pieces by the capacity, and the
+// pieces go round: CTAs are then at neighbouring rows and heads, which for pages lie
+// side by side (32 entries of 16 paged grid heads of 1800 rows: 124 us, even shares
+// 128).
+__device__ __forceinline__ int pair_tiles(const TreeParams &p, int i, int pos) {
+    long long row0;
+    return pos < 0 || pos > p.cap ? 0 : (tree_set_rows(p, p.tc_head[i], pos, 0, row0) + kTile - 1) / kTile;
+}
+__device__ __forceinline__ long long entry_tiles(const TreeParams &p, int b) {
+    const int pos = p.pos[b];
+    if (p.tc_same) return (long long)p.n_tc * pair_tiles(p, 0, pos);
+    long long n = 0;
+    for (int i = 0; i < p.n_tc; ++i) n += pair_tiles(p, i, pos);
+    return n;
+}
+// Sums over the threads before this one, and over all of them (every thread).
+__device__ __forceinline__ void scan_block(Range &r, long long v, int f, long long &v0, int &f0, long long &v_all, int &f_all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+    int y = f;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, x, off);
+        const int c = __shfl_up_sync(0xffffffffu, y, off);
+        if (lane >= off) {
+            x += a;
+            y += c;
+        }
+    }
+    __syncthreads();   // the sums before are read
+    if (lane == 31) {
+        r.sum[warp] = x;
+        r.count[warp] = y;
+    }
+    __syncthreads();
+    v0 = x - v;
+    f0 = y - f;
+    v_all = f_all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) {
+            v0 += r.sum[w];
+            f0 += r.count[w];
+        }
+        v_all += r.sum[w];
+        f_all += r.count[w];
+    }
+}
+__device__ __forceinline__ void find_range(const TreeParams &p, Range &r) {
+    const int tid = threadIdx.x;
+    long long mine = 0, first = 0, total, v0;
+    int none, f0;
+    for (int b = tid; b < p.B; b += kThreads) {
+        const long long n = entry_tiles(p, b);
+        if (b == tid) first = n;
+        mine += n;
+    }
+    scan_block(r, mine, 0, v0, f0, total, none);
+    const long long begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    if (tid == 0) {
+        r.skip = 0;
+        r.tiles = end - begin;
+    }
+    long long before = 0;
+    int listed = 0;
+    for (int b0 = 0; b0 < p.B && before < end; b0 += kThreads) {
+        const int b = b0 + tid;
+        const long long n = b0 == 0 ? first : b < p.B ? entry_tiles(p, b) : 0;
+        long long all = total;   // one round of entries: its sums are there
+        int in_all;
+        if (p.B > kThreads) scan_block(r, n, 0, v0, f0, all, in_all);
+        const long long lo = before + v0;
+        const bool in = n > 0 && lo < end && lo + n > begin;
+        long long none0, none1;
+        scan_block(r, 0, in, none0, f0, none1, in_all);
+        if (in && listed + f0 < kList) r.list[listed + f0] = b;
+        if (in && lo <= begin) r.skip = begin - lo;
+        before += all;
+        listed += in_all;
+    }
+    if (tid == 0) r.n = min(listed, kList);
+    // the barrier that follows makes it visible
+}
+
+// The items of a CTA, in order: its runs of tiles of one pair.  Every role walks
+// the same list.
 struct Items {
-    int u, b, h, slot, tiles;
+    int k, b, i, pos;                 // even shares: place in the list; entry, head's place and position of the next pair
+    long long left, off;              // tiles to come; tiles of the next pair to leave out
+    int u;                            // pieces: the piece
+    int h, pair, tiles, slot;
+    bool first, last;                 // of the pair's items (even shares)
     Keys ks;
-    __device__ __forceinline__ bool next(const TreeParams &p, int total) {
-        for (;; ) {
+    __device__ __forceinline__ void start(const TreeParams &p, const Range &r) {
+        u = (int)blockIdx.x - (int)gridDim.x;
+        if (!p.tc_even) return;
+        k = i = 0;
+        left = r.tiles;
+        off = r.skip;
+        b = left > 0 ? r.list[0] : 0;
+        pos = left > 0 ? p.pos[b] : 0;
+    }
+    __device__ __forceinline__ bool next_piece(const TreeParams &p) {
+        const int total = p.B * p.tc_items_per_b;
+        for (;;) {
+            if (u >= total - (int)gridDim.x) return false;
             u += gridDim.x;
-            if (u >= total) return false;
             b = u / p.tc_items_per_b;
-            const int it = u % p.tc_items_per_b;
+            const int it = u - b * p.tc_items_per_b;
             int lo = 0, hi = p.n_tc - 1;   // largest i with tc_item0[i] <= it
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (p.tc_item0[mid] <= it) lo = mid; else hi = mid - 1;
             }
             h = p.tc_head[lo];
-            slot = it - p.tc_item0[lo];
-            const int pos = p.pos[b];
-            if (pos < 0 || pos > p.cap || !slab_keys(p, h, pos, 0, slot, ks)) continue;
+            const int piece = it - p.tc_item0[lo];
+            pos = p.pos[b];
+            if (pos < 0 || pos > p.cap || !slab_keys(p, h, pos, 0, piece, ks)) continue;
             tiles = (ks.n + kTile - 1) / kTile;
+            slot = b * p.slots_per_b + p.head[h].slot0 + piece;
+            first = last = false;
             return true;
         }
+    }
+    __device__ __forceinline__ bool next(const TreeParams &p, const Range &r) {
+        if (!p.tc_even) return next_piece(p);
+        while (left > 0) {
+            if (i == p.n_tc) {
+                i = 0;
+                ++k;
+                b = k < r.n ? r.list[k] : b + 1;
+                pos = p.pos[b];
+            }
+            const int n = pair_tiles(p, i, pos);
+            if (off >= n) {
+                off -= n;
+                ++i;
+                continue;
+            }
+            h = p.tc_head[i];
+            pair = b * p.n_tc + i;
+            slot = p.tc_slot0 + pair + (int)blockIdx.x;
+            tiles = (int)min(left, n - off);
+            first = off == 0;
+            last = off + tiles == n;
+            ks.kind = kSlab;
+            const int rows = tree_set_rows(p, h, pos, 0, ks.row0);
+            ks.row0 += off * kTile;
+            ks.n = (int)min((long long)tiles * kTile, rows - off * kTile);
+            left -= tiles;
+            off = 0;
+            ++i;
+            return true;
+        }
+        return false;
     }
 };
 
@@ -150,6 +297,7 @@ struct Shared {
     alignas(16) float nref[kTreeMaxNodes];  // the references, negative; read four at a time
     float corr[kTreeMaxNodes];
     float part[4][kTreeMaxNodes];     // a warp's maxima or sums
+    Range range;
 };
 
 // NP columns of this thread's TMEM lane
@@ -181,7 +329,6 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     allow_next();
-    const int total = p.B * p.tc_items_per_b;
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -204,12 +351,13 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (p.tc_even) find_range(p, sh.range);
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tmem, base = smem_u32(smem);
     Items it;
-    it.u = (int)blockIdx.x - (int)gridDim.x;
+    it.start(p, sh.range);
     bool ok = true;
 
     if (warp == 5) {
@@ -229,7 +377,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                 tc_commit(&sh.pvdone);
                 return true;
             };
-            while (ok && it.next(p, total)) {
+            while (ok && it.next(p, sh.range)) {
                 ok = mbar_wait(&sh.qfull, items & 1, &sh.abort);
                 ++items;
                 for (int t = 0; ok && t < it.tiles; ++t, ++t_all) {
@@ -265,22 +413,28 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         // lane 2 i + x brings half x (64 channels) of box i of a tile
         const int half = lane & 1, first = (lane >> 1) * maps.box;
         int j = 0, items = 0;
-        while (ok && it.next(p, total)) {
+        while (ok && it.next(p, sh.range)) {
             bool bad = false;
+            // the page of the lane's box in a tile, looked up a tile ahead: the next
+            // copies do not wait for it
+            auto page_of = [&](int t) {
+                if (!p.page_table || first >= kTile || t * kTile + first >= it.ks.n) return 0;
+                return p.page_table[(long long)it.b * p.pps + ((unsigned)it.ks.row0 + t * kTile + first) / (unsigned)p.page_rows];
+            };
+            int page = page_of(0);
             for (int t = 0; ok && t < it.tiles; ++t) {
                 const unsigned row = (unsigned)it.ks.row0 + t * kTile + first;
                 int y = (int)row, z = it.b * p.H + it.h;
                 bool on = first < kTile && t * kTile + first < it.ks.n;
                 if (on && p.page_table) {
-                    const unsigned pi = row / (unsigned)p.page_rows;
-                    const int pg = p.page_table[(long long)it.b * p.pps + pi];
-                    y = (int)(row - pi * p.page_rows);
-                    z = pg * p.H + it.h;
-                    if (pg < 0 || pg >= p.num_pages) {
+                    y = (int)(row % (unsigned)p.page_rows);
+                    z = page * p.H + it.h;
+                    if (page < 0 || page >= p.num_pages) {
                         bad = true;
                         on = false;
                     }
                 }
+                page = t + 1 < it.tiles ? page_of(t + 1) : 0;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, on)) * maps.box * 128;
 #pragma unroll 1
                 for (int x = 0; x < 2; ++x, ++j) {
@@ -319,14 +473,17 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             for (int e = tid; e < NP * 16; e += kSoftmax) {
                 const int n = e >> 4, c = e & 15;
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (n < p.N && p.parent[(size_t)b * p.N + n] != RAT_NODE_ABSENT)
+                if (n < p.N) {
+                    const int up = p.parent[(size_t)b * p.N + n];   // at the same time as the query
                     x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (((size_t)b * p.N + n) * p.H + h) * kD + c * 8);
+                    if (up == RAT_NODE_ABSENT) x = make_uint4(0u, 0u, 0u, 0u);
+                }
                 *reinterpret_cast<uint4 *>(smem + kOffQ + (c >> 3) * kQHalf + n * 128 + (((c & 7) ^ (n & 7)) << 4)) = x;
             }
             fence_async();
             mbar_arrive(&sh.qfull);
         };
-        bool more = it.next(p, total);
+        bool more = it.next(p, sh.range);
         if (more) stage_q(it.b, it.h);
         while (more) {
             uint64_t l2[NP / 2];
@@ -445,8 +602,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                 mbar_arrive(&sh.pfull);
             }
             // the item's last scores are in, so Q is free: the next item's go there
-            const int b = it.b, h = it.h, slot = it.slot;
-            more = it.next(p, total);
+            const int pair = it.pair, slot = it.slot;
+            const bool first = it.first, last = it.last;
+            more = it.next(p, sh.range);
             if (more) stage_q(it.b, it.h);
             // sums over the keys: halves of the nodes change lanes until a lane
             // holds NP / 32 nodes' sums over its warp (or two lanes one node's)
@@ -467,7 +625,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
 #pragma unroll
             for (int n = 0; n < (NP + 31) / 32; ++n) sh.part[warp][lane * NP / 32 + n] = l[n];
             softmax_sync();
-            const size_t rowbase = ((size_t)b * p.slots_per_b + p.head[h].slot0 + slot) * p.N;
+            const size_t rowbase = (size_t)slot * p.N;
+            if (tid == 0 && first) p.tc_range[pair].x = (int)blockIdx.x;
+            if (tid == 0 && last) p.tc_range[pair].y = (int)blockIdx.x;
             wait(&sh.copied[items & 3], (items >> 2) & 1);
             wait(&sh.pvdone, (t_all - 1) & 1);
             if (tid < p.N) {
@@ -508,8 +668,7 @@ template <int NP> cudaError_t launch_np(const TreeParams &p, cudaStream_t s) {
     maps.box = p.page_table && p.page_rows < kTile ? p.page_rows : kTile;
     for (int x = 0; x < 2; ++x)
         if (!encode_map_rows(&maps.kv[x], p.cache[x], RAT_BF16, rows, blocks, kD, maps.box)) return cudaErrorInvalidValue;
-    const long long total = (long long)p.B * p.tc_items_per_b;
-    tree_tc_kernel<NP><<<(unsigned)(total < 148 ? total : 148), kThreads, kBytes + 1024, s>>>(p, maps);
+    tree_tc_kernel<NP><<<kTreeTcCtas, kThreads, kBytes + 1024, s>>>(p, maps);
     return cudaGetLastError();
 }
 

@@ -1071,3 +1071,63 @@ def test_a_configuration_changed_in_place_is_seen():
     cfg.dil[1] = 3                              # 62 rows become 63, 64 become 63
     with pytest.raises(ValueError, match="cache_k.*shape"):
         p.step()
+
+
+def ragged(B, top, rng, idle=0.5):
+    """Positions of a server's batch: idle entries, short ones, one long."""
+    pos = np.where(rng.random(B) < idle, 0, rng.integers(1, 200, B))
+    pos[B // 3] = top
+    return [int(x) for x in pos]
+
+
+def test_even_shares_of_a_ragged_batch():
+    # more entries than a CTA has threads, runs of idle ones, CTAs with parts of one long entry and with many short ones
+    rng = np.random.default_rng(11)
+    B, N, cap = 210, 3, 5200
+    cfg = config(B, N, 1, 128, BF16, [1], [0])
+    pos = ragged(B, 2500, rng)
+    pos[100:140] = [0] * 40
+    p = Problem(cfg, cap, pos, random_parents(rng, B, N, 2)).to_gpu()
+    want = p.step()
+    p.check(*want)
+    # entries whose position is out of range are left out, the others keep their results
+    bad = [5, 70, 209]
+    for b, x in zip(bad, (-1, cap + 1, (1 << 31) - 1)):
+        p.d_pos[b] = x
+    o, lse = p.step(check=False)
+    with pytest.raises(rat.RatError, match="RAT_ERR_INVALID"):
+        rat.rat_check_status(p.ws)
+    rest = [b for b in range(B) if b not in bad]
+    assert torch.all(o[bad] == 0) and torch.all(torch.isneginf(lse[bad]))
+    assert (o[rest].float() - want[0][rest].float()).abs().max() <= 2 ** -6     # other shares: other partial sums
+    # nothing held anywhere: no CTA has a tile
+    p = Problem(cfg, cap, [0] * B, random_parents(rng, B, N, 2)).to_gpu()
+    p.check(*p.step())
+
+
+@pytest.mark.parametrize("page_rows", [0, 64])
+@pytest.mark.parametrize("N", [3, 20])
+def test_many_pairs_by_pieces(page_rows, N):
+    rng = np.random.default_rng(12)
+    B, cap = 30, 2400
+    cfg = config(B, N, 16, 128, BF16, [1] * 16, [0, 9] * 8)
+    p = Problem(cfg, cap, ragged(B, 1500, rng, 0.2), random_parents(rng, B, N, 3)).to_gpu()
+    if page_rows:
+        _, _, desc = short_pages(cfg, cap, p, page_rows)
+        p.check(*p.step(desc))
+    else:
+        p.check(*p.step())
+
+
+def test_a_head_without_recurrence_keeps_a_branch_apart():
+    # a = 0: a child of a node with infinities has its own row only, in the step as in the commit
+    for dtype in (F32, BF16):
+        cfg = config(1, 4, 1, 128, dtype, [1], [0], [0])
+        p = Problem(cfg, 64, [9], np.array([[-1, 0, 1, -1]], np.int32))
+        p.k[0, 0], p.v[0, 0] = float("inf"), float("nan")
+        p.to_gpu()
+        o, _ = p.step()
+        assert torch.isfinite(o[0, 3]).all() and torch.isnan(o[0, :3].float()).all()
+        ck, cv = p.ck.clone(), p.cv.clone()
+        commit(p, [2], ck, cv)
+        assert torch.equal(ck[0, 0, 10:12], p.d_k[0, 1:3, 0]) and torch.equal(cv[0, 0, 10:12], p.d_v[0, 1:3, 0])

@@ -392,7 +392,9 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  * for a large bf16 tree step with heads of one dilated set), no other CUDA call
  * after the first on a device: a step can be captured in a
  * CUDA graph and replayed with parents, positions and inputs refreshed in
- * place.  Results do not depend on the order in which the GPU runs the work.
+ * place.  Results do not depend on the order in which the GPU runs the work; in
+ * their last bits they may on the other entries' positions (where one entry's
+ * rows are cut depends on how many there are in all).
  */
 RAT_API rat_status rat_tree_decode_step(const rat_cfg *cfg, const void *q, const void *k, const void *v,
                                         const void *g, const int32_t *parent, const float *state_k,

@@ -126,8 +126,9 @@ struct Range {
     int count[kThreads / 32];
 };
 
-// All tiles of all pairs (b, h), in that order, are dealt out evenly: CTA c of G has
-// tiles total * c / G .. total * (c + 1) / G - 1, whatever the positions.  (Pieces
+// All tiles of all pairs (b, h), in that order, are dealt out evenly: CTA c of G
+// (of as many as there are tiles, if they are fewer) has tiles total * c / G ..
+// total * (c + 1) / G - 1, whatever the positions.  (Pieces
 // of equal length planned by the capacity left CTAs idle where entries are
 // shorter: 16 x 64 nodes over 16000 dense rows 366 -> 333 us.)
 // With many pairs (tree_plan) each is cut into pieces by the capacity, and the
@@ -188,7 +189,9 @@ __device__ __forceinline__ void find_range(const TreeParams &p, Range &r) {
         mine += n;
     }
     scan_block(r, mine, 0, v0, f0, total, none);
-    const long long begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    // no more CTAs than tiles: those between a pair's first and last all have some of it
+    const long long ctas = max(1LL, min((long long)gridDim.x, total)), c = min((long long)blockIdx.x, ctas);
+    const long long begin = total * c / ctas, end = total * min(c + 1, ctas) / ctas;
     if (tid == 0) {
         r.skip = 0;
         r.tiles = end - begin;

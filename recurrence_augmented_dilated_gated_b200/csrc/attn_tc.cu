@@ -1346,20 +1346,6 @@ bool encode_map_tokens(CUtensorMap *map, const void *base, int dtype, int B, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_map_rows(CUtensorMap *map, const void *base, int dtype, long long rows, long long blocks, int d, int box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t e = dtype == RAT_BF16 ? 2 : 4;
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)blocks};
-    const cuuint64_t strides[2] = {e * d, e * d * rows};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, dtype == RAT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t attn_tc_smem_bytes(int hd) {
     const size_t need = (hd == 128 ? (size_t)Smem<128>::kBytes : (size_t)Smem<64>::kBytes) + 1024;
     return need > 120 * 1024 ? need : 120 * 1024;

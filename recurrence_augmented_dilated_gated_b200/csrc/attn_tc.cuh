@@ -69,8 +69,5 @@ bool encode_map_5d(CUtensorMap *map, const void *base, int B, int T, int Ts, int
 // box rows past n read as zero.
 bool encode_map_res(CUtensorMap *map, const void *base, int B, int Ts, int H, int d, int D, int r0, int nres, int n,
                     int box_rows);
-// 3-D map (d, rows, blocks) of a [blocks, rows, d] tensor, box (128 bytes of
-// channels, box_rows, 1), 128-byte swizzle
-bool encode_map_rows(CUtensorMap *map, const void *base, int dtype, long long rows, long long blocks, int d, int box_rows);
 
 }  // namespace rat

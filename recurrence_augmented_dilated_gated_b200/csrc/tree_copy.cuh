@@ -8,6 +8,10 @@
 
 namespace rat {
 
+// 3-D map (d, rows, blocks) of a [blocks, rows, d] tensor, box (128 bytes of
+// channels, box_rows, 1), 128-byte swizzle (tree_maps.cu); false: the driver refused
+bool encode_map_rows(CUtensorMap *map, const void *base, int dtype, long long rows, long long blocks, int d, int box_rows);
+
 constexpr long long kTreeWaitNs = 2000000000LL;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

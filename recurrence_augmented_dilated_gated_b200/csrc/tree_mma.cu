@@ -24,7 +24,6 @@
 // Bound: HBM for small node counts (a row's bytes serve 4 d operations a node);
 // with more than 16 nodes on the same rows the instruction rate, which is why
 // tree_tc.cu takes those where it can.
-#include "attn_tc.cuh"
 #include "tree_keys.cuh"
 
 namespace rat {

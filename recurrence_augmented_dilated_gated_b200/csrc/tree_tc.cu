@@ -30,7 +30,6 @@
 //
 // Every wait is bounded (globaltimer); on expiry the CTA records
 // RAT_ERR_TIMEOUT, drains its copies and instructions, frees its TMEM, exits.
-#include "attn_tc.cuh"
 #include "tmem_io.cuh"
 #include "tree_copy.cuh"
 #include "tree_keys.cuh"

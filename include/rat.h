@@ -44,7 +44,8 @@
  *     allocates no device memory and may be called from several host threads
  *     on different workspaces.  Its only process-wide state is a launch
  *     counter, a per-thread last-error string, each kernel's shared-memory
- *     limit (raised once per device), and the static scratch of
+ *     limit (raised once per device), whether a device takes a cluster of
+ *     sixteen CTAs, the driver's tensor-map encoder, and the static scratch of
  *     rat_decode_step_noalloc.  Calls are asynchronous on `stream`; inputs
  *     must stay valid until the stream reaches the call.
  *   - Workspace: `ws` is caller-allocated device memory of at least

@@ -160,3 +160,23 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
 def test_status_string_of_the_page_error(lib):
     assert lib.rat_status_string(rat.RAT_ERR_NO_PAGES).decode().startswith("RAT_ERR_NO_PAGES")
     assert rat.STATUS_NAMES[rat.RAT_ERR_NO_PAGES] == "RAT_ERR_NO_PAGES"
+
+
+def test_native_part_of_the_binding():
+    # it accepts CUDA tensors that are as planned and leaves everything else to Python
+    from recurrence_augmented_dilated_gated_b200 import _binding
+
+    t, plan = torch.zeros(3, dtype=torch.int32), (("t", torch.int32, (3,), False),)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    assert _binding.pointers(plan, ws, t) is None
+    for odd in (None, 3, "x", [1], torch.nn.Parameter(torch.zeros(3))):
+        assert _binding.pointers(plan, ws, odd) is None
+        assert _binding.pointers(plan, odd, t) is None
+    for bad in ((), (3,), ("t",), (("t", torch.int32, (3,)),)):
+        if len(bad) == 1:
+            assert _binding.pointers(bad, ws, t) is None
+        else:
+            with pytest.raises(TypeError):
+                _binding.pointers(bad, ws, t)
+    with pytest.raises(TypeError):
+        _binding.pointers(plan)

@@ -166,10 +166,12 @@ int piece_target(const SetRows *kinds, int n_kinds, long long B, int at_once, in
 TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     constexpr int kSetsGuess = 8, kSMs = 148;
     // tree_tc.cu takes heads whose nodes all read the same rows, from this many held
-    // rows (by capacity) on.  Both forms measured warm, 16 heads: 0.5 M rows, 8 / 24
-    // / 48 nodes, tree_tc 71 / 98 / 128 us, tree_mma 64 / 76 / 123; 1 M rows 131 /
-    // 156 / 188 against 133 / 146 / 235; 2 M rows 164 / 191 / 229 against 175 / 202 / 363.
-    constexpr long long kTcMinRows = 1 << 20;
+    // tree_tc.cu takes heads whose nodes all read the same rows, from this many held
+    // rows (by capacity) on.  Both forms measured warm, 16 heads, 8 / 24 / 48 nodes:
+    // 1 x 16000 positions (0.24 M rows) tree_tc 43 / 68 / 83 us, tree_mma 39 / 47 / 69;
+    // 4 x 8000 (0.49 M) 59 / 81 / 90 against 59 / 75 / 112; 4 x 16000 (0.98 M) 96 / 115 /
+    // 123 against 104 / 129 / 207; 8 x 16000 (1.95 M) 159 / 180 / 185 against 178 / 220 / 344.
+    const long long kTcMinRows = c->T > 32 ? 3 << 17 : 3 << 18;
     const bool grid = (c->flags & RAT_FLAG_GRID_DILATION) != 0;
     const int N = c->T;
     auto sets_of = [&](int D) {

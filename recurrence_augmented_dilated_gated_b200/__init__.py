@@ -385,9 +385,11 @@ def rat_decode_step_paged(cfg, q, k, v, g, state_k, state_v, cache, cache_cap, p
 
 
 # The raw handle of a device's current stream without building a Stream object
-# (3 us of a 20 us call); the public way where torch has no such function.
+# (3 us of a 20 us call), and the current device without the check that CUDA is
+# initialised (a tensor is there); the public way where torch has no such function.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 _native = None
 
@@ -420,12 +422,12 @@ def _pointers(plan, ws, tensors):
 def _launch(what, p, args, stream):
     """Call entry point `what` on the device of its tensors; `p` from _pointers."""
     ws, ws_bytes, index = p[-3:]
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
         if stream.device.index != index:
             raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, index))
         stream = stream.cuda_stream
     fn = getattr(_lib or load_library(), what)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, ws, ws_bytes, _raw_stream(index) if stream is None else int(stream))
     else:
         with torch.cuda.device(index):

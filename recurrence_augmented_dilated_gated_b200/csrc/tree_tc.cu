@@ -30,6 +30,8 @@
 //
 // Every wait is bounded (globaltimer); on expiry the CTA records
 // RAT_ERR_TIMEOUT, drains its copies and instructions, frees its TMEM, exits.
+#include <float.h>
+
 #include "tmem_io.cuh"
 #include "tree_copy.cuh"
 #include "tree_keys.cuh"
@@ -538,7 +540,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                     softmax_sync();
                     if (tid < NP) {
                         float mx = fmaxf(fmaxf(sh.part[0][tid], sh.part[1][tid]), fmaxf(sh.part[2][tid], sh.part[3][tid]));
-                        if (mx == -INFINITY) mx = 0.f;   // nothing but scores of -inf: they weigh nothing
+                        // nothing but scores of -inf so far: they weigh nothing beside any
+                        // reference, and the first that is more raises this one
+                        mx = fmaxf(mx, -FLT_MAX);
                         const float old = -sh.nref[tid];
                         const bool up = t == 0 || mx > old + kSlack;
                         sh.corr[tid] = t > 0 && up ? exp2f(old - mx) : 1.f;

@@ -54,10 +54,15 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = big + small, big with the 11 bits of tf32 (the instruction cuts small to as many)
-__device__ __forceinline__ void split(uint32_t x, uint32_t &big, uint32_t &small) {
+// x = big + small, big with the 11 bits of tf32 (the instruction cuts small to as many).
+// kInf: an infinity is the largest tf32 and an infinite small part, so that a product
+// of halves has its sign; else it is (infinity, NaN).  The conversion that saturates
+// took 441 us where this one takes 411 (16 x 8 nodes, 16 heads of 4000 rows), so an
+// item uses it when its sums came out not finite, and is taken again.
+template <bool kInf> __device__ __forceinline__ void split(uint32_t x, uint32_t &big, uint32_t &small) {
     uint32_t b;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(b) : "f"(__uint_as_float(x)));
+    if (kInf) asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(b) : "f"(__uint_as_float(x)));
+    else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(b) : "f"(__uint_as_float(x)));
     small = __float_as_uint(__uint_as_float(x) - __uint_as_float(b));
     big = b;
 }
@@ -155,9 +160,9 @@ __device__ __noinline__ void count_keys(Shared &sh, int n_nodes, int k0, bool no
 // sh.nodes.  One body serves slabs and local items (what differs is where a row
 // is and which tiles carry a mask): a second copy of it would only thrash the
 // instruction cache.
-// False when a wait gave up.
-template <typename T, int D>
-__device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, Shared &sh, uint8_t *ring, const Keys *parts,
+enum ItemEnd { kDone, kGaveUp, kAgain };   // a wait gave up; nothing written, to be taken again with kInf
+template <typename T, int D, bool kInf>
+__device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &maps, Shared &sh, uint8_t *ring, const Keys *parts,
                                          int n_parts, int b, int h, int pos, int slot, int &fills) {
     using S = Shape<T, D>;
     constexpr int kTile = S::kTile, kStages = S::kStages, kBlock = S::kBlock, NB = kBlock / 8;
@@ -251,10 +256,10 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
         for (int e = tid; e < WM * 16 * S::kChunks; e += kThreads) {
             uint4 *big = x + S::at(e / S::kChunks, e % S::kChunks, q_rows) / 16, *small = big + q_rows * D / 4;
             const uint4 v = *big;
-            split(v.x, big->x, small->x);
-            split(v.y, big->y, small->y);
-            split(v.z, big->z, small->z);
-            split(v.w, big->w, small->w);
+            split<kInf>(v.x, big->x, small->x);
+            split<kInf>(v.y, big->y, small->y);
+            split<kInf>(v.z, big->z, small->z);
+            split<kInf>(v.w, big->w, small->w);
         }
         __syncthreads();
     }
@@ -320,7 +325,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
                     mbar_wait(&sh.full[q % kStages], (q / kStages) & 1, &never);
             }
             __syncthreads();
-            return false;
+            return kGaveUp;
         }
         if (masked) {
             count_keys<kTile>(sh, n_nodes, k0, ks.kind == kNodes, pos - (int)ks.row0, ks.n, pos, p.head[h].win, p.head[h].dil, p.dedupe, p.grid);
@@ -364,10 +369,10 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
                             ldsm4(as, sq_small + S::at(qr, 4 * k + 2 * y + qc, q_rows));
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) split(ab[i], ab[i], as[i]);
+                            for (int i = 0; i < 4; ++i) split<kInf>(ab[i], ab[i], as[i]);
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) split(f[2 * y + i], bb[i], bs[i]);
+                        for (int i = 0; i < 2; ++i) split<kInf>(f[2 * y + i], bb[i], bs[i]);
                         mma1688(part[y][0], ab, bb[0], bb[1]);
                         mma1688(part[y][1], as, bb[0], bb[1]);
                         mma1688(part[y][2], ab, bs[0], bs[1]);
@@ -446,7 +451,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
                 // the instruction's key index x is key 2 x, x + 4 key 2 x + 1: P's own order
                 uint32_t ab[4], as[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split(__float_as_uint(s[0][(i >> 1) + 2 * (i & 1)]), ab[i], as[i]);
+                for (int i = 0; i < 4; ++i) split<false>(__float_as_uint(s[0][(i >> 1) + 2 * (i & 1)]), ab[i], as[i]);
                 const int vr = kb * 8 + c0;
                 const uint8_t *v = stage + S::kHalf + ((lane >> 2) & 3) * 4;
 #pragma unroll
@@ -454,8 +459,8 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
                     const int c = 2 * i + (lane >> 4);
                     float t[4] = {};
                     uint32_t bb[2], bs[2];
-                    split(*reinterpret_cast<const uint32_t *>(v + S::at(vr, c)), bb[0], bs[0]);
-                    split(*reinterpret_cast<const uint32_t *>(v + S::at(vr + 1, c)), bb[1], bs[1]);
+                    split<kInf>(*reinterpret_cast<const uint32_t *>(v + S::at(vr, c)), bb[0], bs[0]);
+                    split<kInf>(*reinterpret_cast<const uint32_t *>(v + S::at(vr + 1, c)), bb[1], bs[1]);
                     mma1688(t, as, bb[0], bb[1]);
                     mma1688(t, ab, bs[0], bs[1]);
                     mma1688(t, ab, bb[0], bb[1]);
@@ -478,7 +483,21 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
         }
     }
     cp_wait<0>();
-    __syncthreads();
+    if constexpr (S::kF32 && !kInf) {
+        // a sum that is not finite, of a node that is there
+        bool odd = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float z = l[u] * 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) z = fmaf(o[i][2 * u], 0.f, fmaf(o[i][2 * u + 1], 0.f, z));
+            const int r = wm * 16 + r0 + 8 * u;
+            odd |= z != z && r < n_nodes && sh.ti.depth[sh.nodes[min(r, kTreeMaxNodes - 1)]] >= 0;
+        }
+        if (__syncthreads_or(odd)) return kAgain;
+    } else {
+        __syncthreads();
+    }
     float *so = reinterpret_cast<float *>(ring);   // [warp][16][D], a row's columns turned by 8 r (banks)
     float M[2], L[2];
 #pragma unroll
@@ -560,7 +579,7 @@ __device__ __forceinline__ bool run_item(const TreeParams &p, const Maps &maps, 
             IO4<T>::store(static_cast<T *>(p.o) + (((size_t)b * p.N + r) * p.H + h) * D + c, x);
         }
     }
-    return true;
+    return kDone;
 }
 
 template <typename T, int D>
@@ -615,7 +634,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
             __syncthreads();
             if (tid < 32) list_nodes(p, sh.ti, h, x % sets, sh.nodes, &sh.n);
         }
-        if (!run_item<T, D>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills)) break;
+        ItemEnd end = run_item<T, D, false>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
+        if constexpr (sizeof(T) == 4) {
+            if (end == kAgain) end = run_item<T, D, true>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
+        }
+        if (end == kGaveUp) break;
     }
     // this kernel ends after the one before it (tree_tc.cu's part of the step),
     // so that the one after, which waits for this one, has both

@@ -120,7 +120,8 @@ template <typename T> __device__ __forceinline__ void tree_gate(float g, float &
     if constexpr (sizeof(T) == 4) {
         gate_pair(g, a, oma);
     } else {
-        const float e = exp2f_fast(fminf(g * -1.44269504f, 115.f));   // e^80: an infinity times 0 would be NaN
+        // logits beyond +-80 saturate: an infinity times a gate of 0 would be NaN
+        const float e = exp2f_fast(fmaxf(fminf(g * -1.44269504f, 115.f), -115.f));
         a = __fdividef(1.f, 1.f + e);
         oma = e * a;
     }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from parity import f64
-from test_gpu_tree import BF16, DEV, F32, Problem, config, random_parents
+from test_gpu_tree import BF16, DEV, F32, Problem, commit, config, random_parents
 
 rat = pytest.importorskip("recurrence_augmented_dilated_gated_b200")
 
@@ -52,3 +52,21 @@ def test_infinities_in_held_rows(dtype, d, D, W, N):
         assert np.abs(off).max() <= 1e-4
     else:
         assert np.linalg.norm(off) <= 1e-2 * np.linalg.norm(ro[~hit])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sep", [0, 1])
+def test_an_infinite_token_behind_a_saturated_gate(dtype, d, sep):
+    # logits beyond +-80 saturate, 1 - a included: an infinite value times it is infinite, in the step as in the commit
+    for g in (100.0, 1000.0, float("inf")):
+        cfg = config(1, 2, 1, d, dtype, [1], [0], sep=sep)
+        p = Problem(cfg, 64, [9], np.array([[-1, 0]], np.int32))
+        (p.g[1] if sep else p.g)[0, 0], p.v[0, 0, 0, 3], p.v[0, 0, 0, 4] = g, float("inf"), -float("inf")
+        p.to_gpu()
+        o, _ = p.step()
+        _, state, _ = commit(p, [1], p.ck, p.cv)
+        want = torch.zeros(d, device=DEV)
+        want[3], want[4] = float("inf"), -float("inf")
+        for x in (o[0, 0, 0].float(), o[0, 1, 0].float(), state[0, 0]):
+            assert torch.equal(torch.where(torch.isfinite(x), torch.zeros_like(x), x), want)

@@ -504,6 +504,8 @@ RAT_API long long rat_launch_count(void);
  * rat_debug_set_scan_stall makes scan chunk `ticket` (0-based launch order;
  * -1 = off) never publish its carry, so the chunks after it must give up after
  * `spin_limit_ns` (0 = the default of one second) and record RAT_ERR_TIMEOUT.
+ * In the workspace of a tree step, CTA `ticket` of its kernels never sees the
+ * first tile that it fetches by TMA complete, and its waits give up likewise.
  * Stored in the workspace header; no effect on other workspaces.
  */
 RAT_API rat_status rat_debug_set_scan_stall(void *ws, size_t ws_bytes, int64_t ticket, int64_t spin_limit_ns,

@@ -12,8 +12,6 @@ namespace rat {
 // channels, box_rows, 1), 128-byte swizzle (tree_maps.cu); false: the driver refused
 bool encode_map_rows(CUtensorMap *map, const void *base, int dtype, long long rows, long long blocks, int d, int box_rows);
 
-constexpr long long kTreeWaitNs = 2000000000LL;
-
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -41,19 +39,49 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity) {
         : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
-// False when the wait gave up or another role has.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    const unsigned long long t0 = global_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort_flag) return false;
-            if ((long long)(global_ns() - t0) > kTreeWaitNs) return false;
-        }
-    }
+// The waits of a CTA (shared memory): how long one may take, in ns, and whether a role
+// gave up.  32 bits of the timer: a wait of more than two seconds is cut to that.
+struct Waits {
+    unsigned limit;
+    volatile int abort;
+};
+__device__ __forceinline__ unsigned global_ns_lo() {
+    unsigned t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
+// What the workspace's header says of them (as of the scan's): read where a kernel
+// begins, used by the same thread once its first barrier is past, when the values have
+// come (waiting for them before it took 2 us of a step of 423).  With failure injection the
+// CTA's first tile, `bar`, awaits bytes that do not come.
+struct WaitSettings {
+    long long limit, stall;
+};
+__device__ __forceinline__ WaitSettings start_waits(Waits &w, const WsHeader *hdr) {
+    w.limit = (unsigned)kDefaultSpinNs;
+    w.abort = 0;
+    return {hdr->spin_limit_ns, hdr->stall_ticket_plus1};
+}
+__device__ __forceinline__ void set_waits(Waits &w, const WaitSettings &s, uint64_t *bar) {
+    if (s.limit > 0) w.limit = (unsigned)min(s.limit, 2000000000LL);
+    if (s.stall == (long long)blockIdx.x + 1)
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], 16;" ::"r"(smem_u32(bar)) : "memory");
+}
+// False when the wait gave up or another role of the CTA has.
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, Waits *w) {
+    const unsigned t0 = global_ns_lo();
+    while (!mbar_try(bar, parity))
+        if (w->abort || global_ns_lo() - t0 > w->limit) return false;
+    return true;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, Waits *w) {
+    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, w);
+}
+// For what is in flight when a CTA gives up: the default limit, and nothing ends it early.
+static __device__ __noinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try(bar, parity))
+        if ((long long)(global_ns() - t0) > kDefaultSpinNs) return;
 }
 // orders this thread's ordinary accesses to shared memory before later TMA and
 // tcgen05 accesses (with the barrier that follows)

@@ -112,7 +112,7 @@ struct Shared {
     int nodes[kTreeMaxNodes];
     int n, bad, odd;                      // odd: some local value is not finite
     uint64_t full[kStagesMax];              // a slab's tile has landed
-    volatile int abort;
+    Waits waits;
     uint8_t count[kTreeMaxNodes][kTileMax];  // how often a key of a masked tile counts for a node
     float m[kWarps][16], l[kWarps][16];
     float inv[kTreeMaxNodes];
@@ -283,7 +283,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
     for (int t = 0; t < n_tiles; ++t) {
         const int f = fill0 + t;
         uint8_t *stage = ring + (f % kStages) * S::kStage;
-        if (t < bulk) ok = mbar_wait(&sh.full[f % kStages], (f / kStages) & 1, &sh.abort);
+        if (t < bulk) ok = mbar_wait(&sh.full[f % kStages], (f / kStages) & 1, &sh.waits);
         else cp_wait<kStages - 2>();
         const uint32_t sk = smem_u32(stage), sv = sk + S::kHalf;
         int k0;
@@ -320,10 +320,10 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
         if (!__syncthreads_and(ok)) {
             if (tid == 0) {
                 report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
-                volatile int never = 0;
-                for (int q = f; q < fill0 + min(bulk, t + kStages - 1); ++q)   // copies in flight
-                    mbar_wait(&sh.full[q % kStages], (q / kStages) & 1, &never);
+                static_assert(kStages == 2, "this tile's copies are the only ones in flight");
+                mbar_drain(&sh.full[f % kStages], (f / kStages) & 1);
             }
+            cp_wait<0>();
             __syncthreads();
             return kGaveUp;
         }
@@ -596,9 +596,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
         TreeWalk<T, D>::ask_queries(p, b, h);
     }
     const int pos = p.pos[b];
+    WaitSettings waits = {};
     if (tid == kThreads - 1) {
         for (int i = 0; i < kStagesMax; ++i) mbar_init(&sh.full[i], 1);
-        sh.abort = 0;
+        waits = start_waits(sh.waits, p.hdr);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     int fills = 0;
@@ -609,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
     }
     if (tid >= 32 && tid < 32 + kTreeMaxNodes) sh.parent[tid - 32] = tid - 32 < p.N ? p.parent[(size_t)b * p.N + tid - 32] : RAT_NODE_ABSENT;
     __syncthreads();
+    if (tid == kThreads - 1) set_waits(sh.waits, waits, &sh.full[0]);
     if (li == 0) tell_pieces(p, sh.ti, b, h, pos);
     if (!sh.ti.valid || sh.ti.max_depth < 0) {
         if (!sh.ti.valid && li == 0 && tid == 0) report_error(p.hdr, RAT_ERR_INVALID, b);

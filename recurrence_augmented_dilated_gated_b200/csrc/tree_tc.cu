@@ -295,7 +295,8 @@ struct Items {
 struct Shared {
     uint64_t full[kSlotsMax], empty[kSlotsMax], sfull[2], sempty[2], qfull, pfull, pvdone, copied[4], drain;
     uint32_t tmem;
-    volatile int abort;
+    Waits waits;
+    int asked;                        // K~ and V~ tiles that the copies have been asked for
     int bad[4];                       // item number + 1 of an item with an invalid page, by item mod 4 (the copies
                                       // run at most three items ahead of the softmax, as does copied)
     alignas(16) float nref[kTreeMaxNodes];  // the references, negative; read four at a time
@@ -333,6 +334,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     allow_next();
+    WaitSettings waits = {};
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -347,8 +349,8 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         mbar_init(&sh.pvdone, 1);
         for (int i = 0; i < 4; ++i) mbar_init(&sh.copied[i], 32);
         mbar_init(&sh.drain, 1);
-        sh.abort = 0;
         for (int i = 0; i < 4; ++i) sh.bad[i] = 0;
+        waits = start_waits(sh.waits, p.hdr);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 5) {
@@ -359,6 +361,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     tc_before();
     __syncthreads();
     tc_after();
+    if (tid == 0) set_waits(sh.waits, waits, &sh.full[0]);
     const uint32_t tmem = sh.tmem, base = smem_u32(smem);
     Items it;
     it.start(p, sh.range);
@@ -372,7 +375,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             const uint32_t iqk = idesc(NP, false), ipv = idesc(NP, true);
             auto product = [&](int t) {   // O^T += V~^T P^T of tile t
                 const int s = pv_slot % kSlots;
-                if (!mbar_wait(&sh.full[s], (pv_slot / kSlots) & 1, &sh.abort) || !mbar_wait(&sh.pfull, t & 1, &sh.abort)) return false;
+                if (!mbar_wait(&sh.full[s], (pv_slot / kSlots) & 1, &sh.waits) || !mbar_wait(&sh.pfull, t & 1, &sh.waits)) return false;
                 tc_after();
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
@@ -382,12 +385,12 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                 return true;
             };
             while (ok && it.next(p, sh.range)) {
-                ok = mbar_wait(&sh.qfull, items & 1, &sh.abort);
+                ok = mbar_wait(&sh.qfull, items & 1, &sh.waits);
                 ++items;
                 for (int t = 0; ok && t < it.tiles; ++t, ++t_all) {
                     const int s = j % kSlots;
-                    ok = mbar_wait(&sh.full[s], (j / kSlots) & 1, &sh.abort) &&
-                         (t_all < 2 || mbar_wait(&sh.sempty[t_all & 1], (t_all / 2 - 1) & 1, &sh.abort));
+                    ok = mbar_wait(&sh.full[s], (j / kSlots) & 1, &sh.waits) &&
+                         (t_all < 2 || mbar_wait(&sh.sempty[t_all & 1], (t_all / 2 - 1) & 1, &sh.waits));
                     if (!ok) break;
                     tc_after();
 #pragma unroll
@@ -404,12 +407,11 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             }
             if (ok && pv_slot >= 0) ok = product(t_all - 1);
             if (!ok) {
-                sh.abort = 1;
+                sh.waits.abort = 1;
                 report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
             }
             tc_commit(&sh.drain);   // everything issued has finished before TMEM is freed
-            volatile int never = 0;
-            mbar_wait(&sh.drain, 0, &never);
+            mbar_drain(&sh.drain, 0);
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -443,7 +445,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
 #pragma unroll 1
                 for (int x = 0; x < 2; ++x, ++j) {
                     const int s = j % kSlots;
-                    if (j >= kSlots) ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[s], (j / kSlots - 1) & 1, &sh.abort));
+                    if (j >= kSlots) ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[s], (j / kSlots - 1) & 1, &sh.waits));
                     if (!ok) break;
                     if (lane == 0) mbar_expect(&sh.full[s], bytes);
                     __syncwarp();
@@ -454,12 +456,10 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             mbar_arrive(&sh.copied[items & 3]);
             ++items;
         }
+        if (lane == 0) sh.asked = j;
         if (!ok) {
-            sh.abort = 1;
+            sh.waits.abort = 1;
             if (lane == 0) report_error(p.hdr, RAT_ERR_TIMEOUT, (int)blockIdx.x);
-            volatile int never = 0;
-            for (int q = max(0, j - kSlots); q < j; ++q)   // copies still in flight
-                mbar_wait(&sh.full[q % kSlots], (q / kSlots) & 1, &never);
         }
     } else {
         // ------------------------------------------------ softmax
@@ -468,9 +468,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
         int t_all = 0, items = 0;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (__all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort))) return;
+            if (!ok || __all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.waits))) return;
             ok = false;
-            sh.abort = 1;   // the waits that follow, everyone's, end at once
+            sh.waits.abort = 1;   // the waits that follow, everyone's, end at once
         };
         // queries of an item: row n of Q is node n (absent nodes: zeros)
         auto stage_q = [&](int b, int h) {
@@ -658,6 +658,9 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     }
     tc_before();
     __syncthreads();
+    // whichever role gave up, the copies still in flight land before the CTA leaves
+    if (warp == 4 && sh.waits.abort)
+        for (int q = max(0, sh.asked - kSlots); q < sh.asked; ++q) mbar_drain(&sh.full[q % kSlots], (q / kSlots) & 1);
     if (warp == 5) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

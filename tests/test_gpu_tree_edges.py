@@ -70,3 +70,29 @@ def test_an_infinite_token_behind_a_saturated_gate(dtype, d, sep):
         want[3], want[4] = float("inf"), -float("inf")
         for x in (o[0, 0, 0].float(), o[0, 1, 0].float(), state[0, 0]):
             assert torch.equal(torch.where(torch.isfinite(x), torch.zeros_like(x), x), want)
+
+
+@pytest.mark.parametrize("dtype,d,D,N,cap,pos,ticket", [
+    (BF16, 128, 1, 4, 800000, [2000], 0),          # the persistent form: one tile a CTA, its copies all asked for
+    (BF16, 128, 1, 20, 800000, [60000], 3),        # several tiles a CTA, the ring in use
+    (BF16, 128, 1, 40, 800000, [60000], 3),        # six slots
+    (BF16, 128, 4, 9, 4000, [3000, 2999], 1),      # slabs on the register-fragment form
+    (BF16, 64, 1, 5, 100, [90], 0),               # all of a head's keys in one item
+    (F32, 128, 4, 20, 4000, [3000, 2999], 2),
+    (F32, 64, 1, 40, 110, [70], 0),
+])
+def test_an_expired_wait_is_reported_and_the_workspace_recovers(dtype, d, D, N, cap, pos, ticket):
+    # a tile that never completes: the waits for it run out, the step says so, the next one on that workspace is right
+    B = len(pos)
+    cfg = config(B, N, 1, d, dtype, [D], [0])
+    p = Problem(cfg, cap, pos, random_parents(np.random.default_rng(N), B, N, 5, pad=False)).to_gpu()
+    want = p.step()
+    p.ws[256:] = 0x7f                               # nothing of the step that gives up may depend on what was there
+    rat.rat_debug_set_scan_stall(p.ws, ticket=ticket, spin_limit_ns=20_000_000)
+    p.step(check=False)
+    with pytest.raises(rat.RatError) as e:
+        rat.rat_check_status(p.ws)
+    assert e.value.status == rat.RAT_ERR_TIMEOUT
+    rat.rat_debug_set_scan_stall(p.ws, ticket=-1)
+    o, lse = p.step()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])

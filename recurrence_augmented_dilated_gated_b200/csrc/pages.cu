@@ -65,11 +65,13 @@ __global__ void __launch_bounds__(kThreads, 1) page_update_kernel(const PageUpda
     const int n_free = *p.n_free;
     const unsigned below = (1u << lane) - 1u;
 
-    // state of one entry: bit 0 has, bit 1 needed
+    // state of one entry: bit 0 has, bit 1 needed; with both it stays as it is, and so does
+    // whatever a sequence has whose length is out of range
     auto state = [&](int page, int e, int len) {
+        if (len > p.cap) return 3;
         const int b = p.by_pps.div(e);
         bool need = false;
-        if (len >= 0 && len <= p.cap) {
+        if (len >= 0) {
             const int n = (int)min((long long)len + p.extra, (long long)p.cap);
             const unsigned p0 = (unsigned)(e - b * p.pps) * (unsigned)p.page_rows;
             const long long p1 = (long long)p0 + p.page_rows;
@@ -77,7 +79,6 @@ __global__ void __launch_bounds__(kThreads, 1) page_update_kernel(const PageUpda
             for (int c = 0; c < p.ncls && !need; ++c) need = page_needed(p.cls[c], p.grid, p0, p1, n);
         }
         const bool has = page >= 0 && page < p.num_pages;
-        if (len > p.cap) need = has;   // a length out of range: the entry stays as it is
         return (has ? 1 : 0) | (need ? 2 : 0);
     };
 

@@ -96,3 +96,16 @@ def test_an_expired_wait_is_reported_and_the_workspace_recovers(dtype, d, D, N, 
     rat.rat_debug_set_scan_stall(p.ws, ticket=-1)
     o, lse = p.step()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_an_entry_whose_length_is_out_of_range_keeps_its_table():
+    # every value of it, those that name no page too; the other entries are served
+    cfg = config(2, 1, 1, 64, BF16, [1], [0])
+    ws = rat.workspace(cfg, rat.RAT_OP_STATUS)
+    table = torch.tensor([[3, -7, 99], [0, 1, -1]], dtype=torch.int32, device=DEV)
+    free = torch.tensor([2, 4, 5, 9, 9, 9], dtype=torch.int32, device=DEV)
+    n = torch.tensor([3], dtype=torch.int32, device=DEV)
+    rat.rat_page_table_update(cfg, table, 8, 6, 24, torch.tensor([25, 24], dtype=torch.int32, device=DEV), 0, free, n, ws)
+    with pytest.raises(rat.RatError, match="RAT_ERR_INVALID"):
+        rat.rat_check_status(ws)
+    assert table.tolist() == [[3, -7, 99], [0, 1, 5]] and int(n) == 2 and free[:2].tolist() == [2, 4]

@@ -21,6 +21,8 @@
 //     64-bit mask); a long window is cut into further items.
 // tree_combine_kernel joins the partials in a fixed order.
 // Bound: the cache rows, each read once; 4 d operations per (node, row).
+#include <algorithm>
+
 #include "tree_keys.cuh"
 
 namespace rat {
@@ -228,6 +230,11 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     // entries of 16 heads).
     const long long pairs = (long long)c->B * c->H;
     const long long share = pairs > 0 ? (48ll * kSMs + pairs - 1) / pairs : 1;
+    // Nor more pieces of a head than 96 rounds of one item an SM: a piece has partials of
+    // its own, which would grow with the capacity whatever is held (64 entries of 16 heads
+    // of 2^20 positions, 64 nodes: 8.8 GB, so 0.5).
+    const long long most_pieces = pairs > 0 ? (96ll * kSMs + pairs - 1) / pairs : 1;
+    auto cut = [&](int rows, int length) { return (int)std::min<long long>((rows + length - 1) / length, most_pieces); };
     int ctas = 0, slots = 0, per_head = 0;
     p->n_tc = p->tc_items_per_b = 0;
     p->tc_same = 1;
@@ -237,14 +244,14 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
         const int D = c->dil[h];
         const int slab = (int)(((long long)cap + D - 1) / D);
         const bool one_set = grid || D == 1, by_tc = tc && one_set;
-        const int ns = by_tc && even ? 1 : (slab + (by_tc ? target_tc : target) - 1) / (by_tc ? target_tc : target);
+        const int ns = by_tc && even ? 1 : cut(slab, by_tc ? target_tc : target);
         p->head[h].dil = D;
         // with dedupe a D = 1 head's window keys are all in its dilated set
         p->head[h].win = (c->flags & RAT_FLAG_DEDUPE) && D == 1 ? 0 : c->win[h];
         p->head[h].slab = slab;
         p->head[h].nsplit = ns;
         const int w = p->head[h].win < cap ? p->head[h].win : cap;
-        p->head[h].wsplit = w > window_rows ? (w + window_rows - 1) / window_rows : 1;
+        p->head[h].wsplit = w > window_rows ? cut(w, window_rows) : 1;
         const long long most = (long long)sets_of(D) * ns;
         p->head[h].slab_ctas = (int)(most < share ? most : share);
         p->head[h].fused = 0;

@@ -180,3 +180,15 @@ def test_native_part_of_the_binding():
                 _binding.pointers(bad, ws, t)
     with pytest.raises(TypeError):
         _binding.pointers(plan)
+
+
+def test_workspace_of_many_long_sequences(lib):
+    # partials are bounded by what the GPU runs at a time and by the pairs, not by the capacity
+    for dtype, d, page in ((rat.RAT_BF16, 128, 0), (rat.RAT_F32, 64, 0)):
+        for B in (1, 64, 256, 1000):
+            for win in (0, 1 << 20):
+                c = cfg(B=B, T=64, H=16, d=d, dtype=dtype, dil=[1] * 16, win=[win] * 16)
+                size = lib.rat_workspace_size(c.ref(), rat.RAT_OP_TREE, 1 << 20)
+                pairs = B * 16
+                slots = 2 * (96 * 148 + 2 * pairs)     # pieces of sets and of windows
+                assert size <= (1 << 20) + (slots * 64 * (d + 2) + 3 * pairs * 64 * d) * 4, (B, win, size)

@@ -388,6 +388,7 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  *   state_k/v    in  [B,H,d] fp32, after position pos[b]-1; not changed
  *   cache_k/v    in  as rat_decode_step, rows of positions < pos[b]; not changed
  *   pos          in  DEVICE int32 [B], 0 <= pos[b] <= cache_cap
+ *   cache_cap    < 2^31 - 65536
  *   o            out [B,N,H,d];  lse out [B,H,N] fp32 or NULL
  * ws: rat_workspace_size(cfg, RAT_OP_TREE, cache_cap) bytes.  Two kernels (three
  * for a large bf16 tree step with heads of one dilated set), no other CUDA call

@@ -134,6 +134,8 @@ rat_status check_tree(const rat_cfg *c, int cap) {
 rat_status plan_tree(const rat_cfg *c, int cap, int page_rows, TreeParams *p, TreeLayout *tl) {
     rat_status st = check_tree(c, cap);
     if (st != RAT_OK) return st;
+    // a kernel's row and position arithmetic steps past an end by less than this, in 32 bits
+    if (cap > 0x7fffffff - 0x10000) return fail(RAT_ERR_UNSUPPORTED, "cache_cap %d exceeds 2^31 - 65537", cap);
     *tl = tree_plan(c, cap, page_rows, p);
     const long long most = std::max((long long)std::max(p->ctas_per_b, p->slots_per_b + p->n_tc), (long long)c->H * c->T);
     if ((double)c->B * (double)most >= 2147483647.0 - kTreeTcCtas)

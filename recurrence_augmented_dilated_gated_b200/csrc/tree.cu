@@ -136,6 +136,9 @@ struct SetRows {
     long long sets;
 };
 
+// rows / length, rounded up (rows up to 2^31 - 1)
+int count_pieces(int rows, int length) { return (int)(((long long)rows + length - 1) / length); }
+
 // The longest pieces to cut dilated sets into, for items that run `at_once` at a
 // time and cost as much as `fixed` rows besides their own (a piece's first loads,
 // its join and its partials, 5 us): the least number of rounds times the length
@@ -148,7 +151,7 @@ int piece_target(const SetRows *kinds, int n_kinds, long long B, int at_once, in
         long long items = 0;
         int longest = 0;
         for (int k = 0; k < n_kinds; ++k) {
-            const int pieces = (kinds[k].rows + target - 1) / target, len = (kinds[k].rows + pieces - 1) / pieces;
+            const int pieces = count_pieces(kinds[k].rows, target), len = count_pieces(kinds[k].rows, pieces);
             items += kinds[k].sets * pieces;
             if (len > longest) longest = len;
         }
@@ -234,7 +237,7 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     // its own, which would grow with the capacity whatever is held (64 entries of 16 heads
     // of 2^20 positions, 64 nodes: 8.8 GB, so 0.5).
     const long long most_pieces = pairs > 0 ? (96ll * kSMs + pairs - 1) / pairs : 1;
-    auto cut = [&](int rows, int length) { return (int)std::min<long long>((rows + length - 1) / length, most_pieces); };
+    auto cut = [&](int rows, int length) { return (int)std::min<long long>(count_pieces(rows, length), most_pieces); };
     int ctas = 0, slots = 0, per_head = 0;
     p->n_tc = p->tc_items_per_b = 0;
     p->tc_same = 1;
@@ -287,7 +290,7 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     const size_t elt = c->dtype == RAT_F32 ? 4 : 2;
     TreeLayout L;
     const size_t pairs_tc = even ? (size_t)c->B * p->n_tc : 0, all_slots = (size_t)c->B * slots + (even ? pairs_tc + kTreeTcCtas : 0);
-    p->tc_slot0 = c->B * slots;
+    p->tc_slot0 = (int)((long long)c->B * slots);   // in range, or the step is refused
     L.node_rows = 0;
     L.part = al((size_t)c->B * c->H * 2 * N * c->d * elt);
     L.ml = L.part + al(all_slots * N * c->d * sizeof(float));

@@ -192,3 +192,29 @@ def test_workspace_of_many_long_sequences(lib):
                 pairs = B * 16
                 slots = 2 * (96 * 148 + 2 * pairs)     # pieces of sets and of windows
                 assert size <= (1 << 20) + (slots * 64 * (d + 2) + 3 * pairs * 64 * d) * 4, (B, win, size)
+
+
+MOST_CAP = 2 ** 31 - 2 ** 16 - 1   # of a tree step
+
+
+@pytest.mark.parametrize("dtype", [rat.RAT_BF16, rat.RAT_F32])
+@pytest.mark.parametrize("flags", [0, rat.RAT_FLAG_GRID_DILATION])
+@pytest.mark.parametrize("dil,win", [([1, 1], [0, 0]), ([1, 1], [2 ** 31 - 1, 5]), ([16, 3], [2 ** 31 - 1, 2 ** 31 - 1]),
+                                     ([2 ** 31 - 1, 64], [0, 300])])
+def test_capacities_near_two_to_the_31(lib, dtype, flags, dil, win):
+    # the plan's counts stay in range up to the largest capacity, and what is past it is refused
+    for B, T in ((1, 1), (1, 64), (8, 33)):
+        c = cfg(B=B, T=T, dtype=dtype, flags=flags, dil=dil, win=win)
+        last = 0
+        for cap in (1 << 20, 1 << 28, (1 << 31) - (1 << 20), MOST_CAP):
+            size = lib.rat_workspace_size(c.ref(), rat.RAT_OP_TREE, cap)
+            # a partial of d floats, a maximum and a sum for each node, head and piece, of 128 rows at least
+            assert 0.9 * last <= size <= (1 << 20) + B * T * 2 * 1100 * (cap / 64 + 4), (cap, size)
+            last = size
+        for cap in (MOST_CAP + 1, 2 ** 31 - 4096, 2 ** 31 - 1):
+            assert lib.rat_workspace_size(c.ref(), rat.RAT_OP_TREE, cap) == 0
+            assert step(lib, c, cap=cap) == rat.RAT_ERR_UNSUPPORTED
+        pages = rat.rat_paged_cache(pool_k=P, pool_v=P, page_table=P, page_rows=1 << 16, pages_per_seq=1 << 17, num_pages=4)
+        assert step(lib, c, cap=2 ** 31 - 1, desc=pages) == rat.RAT_ERR_UNSUPPORTED
+        # a commit has no plan: its positions are bounded by the capacity, whatever it is
+        assert commit(lib, c, cap=2 ** 31 - 1, ws=None) == rat.RAT_ERR_INVALID and b"workspace" in lib.rat_last_error()

@@ -474,6 +474,7 @@ RAT_API rat_status rat_page_table_update(const rat_cfg *cfg, int32_t *page_table
  *   ring_slots   out DEVICE int64 [B,T,H] or NULL: under the fixed grid, its
  *                row in the window ring, for the last W_h positions of the run; else -1
  *   cache        NULL for the dense cache; of a paged one, table and sizes are used
+ *   B * T < 2^31 - 128
  * An entry with pos or count out of range ([0, cache_cap]) gets -1 throughout
  * and RAT_ERR_INVALID is recorded.  ws as rat_page_table_update.
  */

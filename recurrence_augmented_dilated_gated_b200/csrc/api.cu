@@ -1057,8 +1057,8 @@ rat_status rat_slot_map(const rat_cfg *cfg, const rat_paged_cache *cache, int ca
     }
     if (cache_cap < 1) return fail(RAT_ERR_INVALID, "cache_cap %d < 1", cache_cap);
     if (empty(&c)) return RAT_OK;
-    if ((double)c.B * c.T >= 2147483647.0 || (double)c.B * ((c.T + 31) / 32) >= 2147483647.0)
-        return fail(RAT_ERR_UNSUPPORTED, "B x T exceeds 2^31 positions");
+    // a CTA has up to 128 positions, and the last one's may pass T
+    if ((long long)c.B * c.T >= 0x80000000LL - 128) return fail(RAT_ERR_UNSUPPORTED, "B x T exceeds 2^31 - 129 positions");
     if (cache_rows(&c, cache_cap) >= 0x7fffffffLL) return fail(RAT_ERR_UNSUPPORTED, "cache rows exceed 2^31");
     CHECK_PTR(pos, "pos"); CHECK_OPT(count, "count"); CHECK_PTR(slots, "slots"); CHECK_OPT(ring_slots, "ring_slots");
     st = check_ws_bytes(ws, ws_bytes, sizeof(WsHeader));

@@ -218,3 +218,12 @@ def test_capacities_near_two_to_the_31(lib, dtype, flags, dil, win):
         assert step(lib, c, cap=2 ** 31 - 1, desc=pages) == rat.RAT_ERR_UNSUPPORTED
         # a commit has no plan: its positions are bounded by the capacity, whatever it is
         assert commit(lib, c, cap=2 ** 31 - 1, ws=None) == rat.RAT_ERR_INVALID and b"workspace" in lib.rat_last_error()
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 100, 2 ** 31 - 128])
+def test_slot_maps_too_wide_for_a_grid_are_refused(lib, T):
+    # ahead of every pointer: the sizes alone decide
+    call = lambda c: lib.rat_slot_map(c.ref(), None, 1000, None, None, None, None, None, 0, None)  # noqa: E731
+    assert call(cfg(B=1, T=T, H=1, dil=[1], win=[0])) == rat.RAT_ERR_UNSUPPORTED
+    assert call(cfg(B=3, T=T // 3 + 1, H=1, dil=[1], win=[0])) == rat.RAT_ERR_UNSUPPORTED
+    assert call(cfg(B=1, T=2 ** 31 - 129, H=1, dil=[1], win=[0])) == rat.RAT_ERR_INVALID and b"pos" in lib.rat_last_error()

@@ -11,6 +11,7 @@ if the library is missing or the tensors are not on a CUDA device.
 """
 import ctypes
 import os
+import warnings
 
 import numpy as np
 import torch
@@ -394,18 +395,30 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _native = None
 
 
+def _native_pointers():
+    """The native check, or one that leaves every call to Python where it is missing or was built for another torch
+    or Python (their objects' layouts are compiled in)."""
+    from .build import binding_target
+
+    try:
+        from . import _binding
+
+        if _binding.built_for == binding_target():
+            return _binding.pointers
+        why = "was built for %s, this is %s" % (_binding.built_for, binding_target())
+    except (ImportError, AttributeError) as e:
+        why = str(e)
+    warnings.warn("_binding.so %s: arguments are checked in Python (7 us a call more); run build.py" % why)
+    return lambda plan, ws, *tensors: None
+
+
 def _pointers(plan, ws, tensors):
     """Addresses of the tensors of a call, then those of its workspace: address, bytes and device index.  `plan` says
     of each tensor (name, dtype, shape or None, may be None).  The usual case is one native call; an argument that it
     does not accept is looked at here, and named if it is wrong."""
     global _native
     if _native is None:
-        path = os.path.join(HERE, "_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError("%s not found: run recurrence_augmented_dilated_gated_b200/build.py" % path)
-        from . import _binding
-
-        _native = _binding.pointers
+        _native = _native_pointers()
     p = _native(plan, ws, *tensors)
     if p is not None:
         return p

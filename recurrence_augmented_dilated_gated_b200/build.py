@@ -2,12 +2,15 @@
 _binding.so (csrc/binding.cpp, the Python binding's native part) with g++.
 
 Both are built in-tree, next to this file, so they ship with the package.
+_binding.so only makes calls shorter on the host: without it the package does
+the same checks in Python, so a failed g++ is a warning.
 """
 import glob
 import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librat.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_STAMP = os.path.join(HERE, "_binding.stamp")   # what BINDING was built for
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -45,16 +49,44 @@ def start_binding(out):
     from torch.utils import cpp_extension
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+    cmd = [os.environ.get("CXX", "g++"), "-DRAT_BUILT_FOR=\"%s\"" % binding_target(), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, BINDING_SOURCE, "-o", out]
     for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", d]
     cmd += ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:
+        warnings.warn("%s: calls take their checks in Python" % e)
+        return None
+
+
+def binding_target():
+    """The torch and the Python whose headers the binding's native part is compiled against."""
+    import torch
+
+    return "torch %s %s %s" % (torch.__version__, sysconfig.get_config_var("SOABI"), torch._C._GLIBCXX_USE_CXX11_ABI)
 
 
 def binding_up_to_date():
-    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(BINDING_SOURCE)
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_STAMP):
+        return False
+    with open(BINDING_STAMP) as f:
+        if f.read() != binding_target():
+            return False
+    return os.path.getmtime(BINDING) >= os.path.getmtime(BINDING_SOURCE)
+
+
+def finish_binding(proc, tmp):
+    out, _ = proc.communicate()
+    if proc.returncode:
+        sys.stderr.write(out.decode())
+        warnings.warn("g++ failed for %s: calls take their checks in Python" % BINDING_SOURCE)
+        return
+    os.replace(tmp, BINDING)
+    with open(BINDING_STAMP + ".tmp%d" % os.getpid(), "w") as f:
+        f.write(binding_target())
+    os.replace(f.name, BINDING_STAMP)
 
 
 def build(force=False, verbose=False, ptxas_v=False):
@@ -64,11 +96,7 @@ def build(force=False, verbose=False, ptxas_v=False):
         binding = start_binding(tmp)
     lib = build_library(force, verbose, ptxas_v)
     if binding:
-        out, _ = binding.communicate()
-        if binding.returncode:
-            sys.stdout.write(out.decode())
-            raise RuntimeError("g++ failed for " + BINDING_SOURCE)
-        os.replace(tmp, BINDING)
+        finish_binding(binding, tmp)
     return lib
 
 

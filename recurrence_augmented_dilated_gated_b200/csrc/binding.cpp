@@ -87,4 +87,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// built_for: the torch and the Python of the headers above (at::Tensor's layout is
+// compiled in), which the caller compares with those that run.
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", RAT_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        m = nullptr;
+    }
+    return m;
+}

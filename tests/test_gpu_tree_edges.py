@@ -109,3 +109,18 @@ def test_an_entry_whose_length_is_out_of_range_keeps_its_table():
     with pytest.raises(rat.RatError, match="RAT_ERR_INVALID"):
         rat.rat_check_status(ws)
     assert table.tolist() == [[3, -7, 99], [0, 1, 5]] and int(n) == 2 and free[:2].tolist() == [2, 4]
+
+
+def test_checks_in_python_give_the_same_calls(monkeypatch):
+    cfg = config(2, 9, 2, 64, BF16, [2, 1], [0, 6])
+    p = Problem(cfg, 300, [250, 5], random_parents(np.random.default_rng(1), 2, 9, 4)).to_gpu()
+    want = p.step()
+    monkeypatch.setattr(rat, "_native", lambda *args: None)
+    got = p.step()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ck = p.ck.clone()
+    commit(p, [8, -1], ck, p.cv.clone())
+    assert not torch.equal(ck.nan_to_num(), p.ck.nan_to_num())
+    with pytest.raises(ValueError, match="pos .*shape"):
+        p.d_pos = p.d_pos[:1]
+        p.step()

@@ -1,6 +1,7 @@
 """Host-side checks of the drafted-tree and page-table entry points (no GPU, nothing is launched): argument errors
 return the documented status before any launch, and workspace sizes are as documented."""
 import ctypes
+import sys
 
 import pytest
 import torch
@@ -227,3 +228,46 @@ def test_slot_maps_too_wide_for_a_grid_are_refused(lib, T):
     assert call(cfg(B=1, T=T, H=1, dil=[1], win=[0])) == rat.RAT_ERR_UNSUPPORTED
     assert call(cfg(B=3, T=T // 3 + 1, H=1, dil=[1], win=[0])) == rat.RAT_ERR_UNSUPPORTED
     assert call(cfg(B=1, T=2 ** 31 - 129, H=1, dil=[1], win=[0])) == rat.RAT_ERR_INVALID and b"pos" in lib.rat_last_error()
+
+
+def test_binding_of_another_torch_is_rebuilt(lib, monkeypatch, tmp_path):
+    assert rat_build.binding_up_to_date()
+    stamp = tmp_path / "stamp"
+    monkeypatch.setattr(rat_build, "BINDING_STAMP", str(stamp))
+    assert not rat_build.binding_up_to_date()                   # not known what it was built for
+    stamp.write_text(rat_build.binding_target())
+    assert rat_build.binding_up_to_date()
+    monkeypatch.setattr(torch, "__version__", "2.0.0")
+    assert not rat_build.binding_up_to_date()
+
+
+@pytest.mark.parametrize("cxx", ["false", "/nonexistent/c++"])
+def test_a_build_without_the_native_part_of_the_binding(lib, monkeypatch, tmp_path, cxx):
+    monkeypatch.setenv("CXX", cxx)
+    for name in ("BINDING", "BINDING_STAMP"):
+        monkeypatch.setattr(rat_build, name, str(tmp_path / name))
+    with pytest.warns(UserWarning, match="in Python"):
+        assert rat_build.build() == rat_build.LIB
+    assert not list(tmp_path.iterdir())
+
+
+class Foreign:
+    built_for = "torch 0.4"
+
+    @staticmethod
+    def pointers(*args):
+        raise AssertionError("called")
+
+
+@pytest.mark.parametrize("module,why", [(None, "halted"), (Foreign, "built for torch 0.4"), (object(), "built_for")])
+def test_checks_in_python_without_the_native_part(lib, monkeypatch, module, why):
+    monkeypatch.setattr(rat, "_native", None)
+    monkeypatch.setitem(sys.modules, rat.__name__ + "._binding", module)
+    monkeypatch.setattr(rat, "_binding", module, raising=False)
+    if module is None:
+        monkeypatch.delattr(rat, "_binding")
+    i, ws = torch.zeros(1, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    with pytest.warns(UserWarning, match=why):
+        with pytest.raises(ValueError, match="CUDA"):
+            rat.rat_slot_map(cfg(B=1, T=4), None, 100, i, None, torch.zeros(1, 4, 2, dtype=torch.int64), None, ws)
+    assert rat._native((), ws) is None                          # looked for once

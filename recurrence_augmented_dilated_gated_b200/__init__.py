@@ -347,9 +347,12 @@ def paged_cache(cfg, pool_k, pool_v, page_table, cache_cap):
     _ptr(page_table, "page_table", torch.int32)
     if page_table.dim() != 2 or page_table.shape[0] != c.B:
         raise ValueError("page_table must be [B, pages_per_seq]")
+    if not pool_k.device == pool_v.device == page_table.device:
+        raise ValueError("pool_k, pool_v and page_table are on different devices")
     desc = rat_paged_cache(pool_k.data_ptr(), pool_v.data_ptr(), page_table.data_ptr(), int(P),
                            int(page_table.shape[1]), int(n))
     desc.device_index, desc.tensors = pool_k.get_device(), (pool_k, pool_v, page_table)   # they live as long as the descriptor
+    desc.made_for = (c.B, c.H, c.d, c.dtype)
     return desc
 
 
@@ -449,12 +452,16 @@ def _launch(what, p, args, stream):
         _check(rc, what)
 
 
-def _paged_desc(cache, index):
-    """The descriptor of a paged cache, its tensors on the call's device."""
+def _paged_desc(cfg, cache, index):
+    """The descriptor of a paged cache, its tensors on the call's device and as large as the call takes them for."""
     if not isinstance(cache, rat_paged_cache):
         raise TypeError("cache must be a rat_paged_cache (paged_cache())")
-    if getattr(cache, "device_index", index) != index:
-        raise ValueError("cache is on cuda:%d, the workspace on cuda:%d" % (cache.device_index, index))
+    c, made = cfg.c, getattr(cache, "made_for", None)
+    if made is not None:
+        if cache.device_index != index:
+            raise ValueError("cache is on cuda:%d, the workspace on cuda:%d" % (cache.device_index, index))
+        if made[0] < c.B or made[1:] != (c.H, c.d, c.dtype):
+            raise ValueError("cache was made for (B, H, d, dtype) = %s, the call has %s" % (made, (c.B, c.H, c.d, c.dtype)))
     return ctypes.byref(cache)
 
 
@@ -506,7 +513,7 @@ def rat_tree_decode_step_paged(cfg, q, k, v, g, parent, state_k, state_v, cache,
     cache_cap = int(cache_cap)
     p = _pointers(_plan(cfg, "paged step", cache_cap, _paged_step_plan), ws,
                   (q, k, v, g, parent, state_k, state_v, pos, o, lse))
-    _launch("rat_tree_decode_step_paged", p, (cfg.ref(), *p[:7], _paged_desc(cache, p[-1]), cache_cap, *p[7:10]), stream)
+    _launch("rat_tree_decode_step_paged", p, (cfg.ref(), *p[:7], _paged_desc(cfg, cache, p[-1]), cache_cap, *p[7:10]), stream)
 
 
 def _commit_plan(cfg, cache_cap, dense=True):
@@ -539,7 +546,7 @@ def rat_tree_commit_paged(cfg, k, v, g, parent, leaf, state_k, state_v, out_stat
     cache_cap = int(cache_cap)
     p = _pointers(_plan(cfg, "paged commit", cache_cap, _paged_commit_plan), ws,
                   (k, v, g, parent, leaf, state_k, state_v, out_state_k, out_state_v, pos, out_pos))
-    _launch("rat_tree_commit_paged", p, (cfg.ref(), *p[:9], _paged_desc(cache, p[-1]), cache_cap, p[9], p[10]), stream)
+    _launch("rat_tree_commit_paged", p, (cfg.ref(), *p[:9], _paged_desc(cfg, cache, p[-1]), cache_cap, p[9], p[10]), stream)
 
 
 def rat_page_table_update(cfg, page_table, page_rows, num_pages, cache_cap, length, extra, free_pages, n_free, ws=None,
@@ -564,7 +571,7 @@ def rat_slot_map(cfg, cache, cache_cap, pos, count, slots, ring_slots=None, ws=N
     plan = (("pos", torch.int32, (c.B,), False), ("count", torch.int32, (c.B,), True),
             ("slots", torch.int64, shape, False), ("ring_slots", torch.int64, shape, True))
     p = _pointers(plan, ws, (pos, count, slots, ring_slots))
-    _launch("rat_slot_map", p, (cfg.ref(), None if cache is None else _paged_desc(cache, p[-1]), int(cache_cap),
+    _launch("rat_slot_map", p, (cfg.ref(), None if cache is None else _paged_desc(cfg, cache, p[-1]), int(cache_cap),
                                 *p[:4]), stream)
 
 

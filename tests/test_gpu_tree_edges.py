@@ -124,3 +124,28 @@ def test_checks_in_python_give_the_same_calls(monkeypatch):
     with pytest.raises(ValueError, match="pos .*shape"):
         p.d_pos = p.d_pos[:1]
         p.step()
+
+
+def test_a_paged_cache_of_other_sizes_is_refused():
+    # on the host, before anything is launched: the kernels would read past a smaller table or pool
+    cfg = config(2, 5, 2, 64, BF16, [2, 1], [0, 6])
+    p = Problem(cfg, 60, [50, 5], random_parents(np.random.default_rng(1), 2, 5, 4)).to_gpu()
+    pools = [torch.zeros(8, 2, 16, 64, dtype=BF16, device=DEV) for _ in range(2)]
+    table = torch.arange(8, dtype=torch.int32, device=DEV).view(2, 4)
+    p.step(rat.paged_cache(cfg, *pools, table, p.cap))
+    slots = torch.empty(2, 5, 2, dtype=torch.int64, device=DEV)
+    for kw, pool, tab in ((dict(B=1), (8, 2, 16, 64), (1, 4)), (dict(H=1, dil=[2], win=[0]), (8, 1, 16, 64), (2, 4)),
+                          (dict(d=128), (8, 2, 16, 128), (2, 4)), (dict(dtype=F32), (8, 2, 16, 64), (2, 4))):
+        other = cfg.replace(**kw)
+        made = rat.paged_cache(other, *(torch.zeros(pool, dtype=other.torch_dtype, device=DEV) for _ in range(2)),
+                               torch.zeros(tab, dtype=torch.int32, device=DEV), p.cap)
+        for call in (lambda: p.step(made), lambda: commit(p, [0, 0], None, None, desc=made),
+                     lambda: rat.rat_slot_map(cfg, made, p.cap, p.d_pos, None, slots, None, p.ws)):
+            with pytest.raises(ValueError, match="made for"):
+                call()
+    # the first entries of a larger table are a table
+    small = cfg.replace(B=1)
+    ws, o = rat.workspace(small, rat.RAT_OP_TREE, p.cap), torch.empty_like(p.d_q[:1])
+    rat.rat_tree_decode_step_paged(small, *(x[:1] for x in (p.d_q, p.d_k, p.d_v, p.d_g, p.d_parent, p.d_sk, p.d_sv)),
+                                   rat.paged_cache(cfg, *pools, table, p.cap), p.cap, p.d_pos[:1], o, None, ws)
+    rat.rat_check_status(ws)

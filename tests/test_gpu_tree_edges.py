@@ -149,3 +149,22 @@ def test_a_paged_cache_of_other_sizes_is_refused():
     rat.rat_tree_decode_step_paged(small, *(x[:1] for x in (p.d_q, p.d_k, p.d_v, p.d_g, p.d_parent, p.d_sk, p.d_sv)),
                                    rat.paged_cache(cfg, *pools, table, p.cap), p.cap, p.d_pos[:1], o, None, ws)
     rat.rat_check_status(ws)
+
+
+@pytest.mark.parametrize("N", [8, 20, 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["k", "v", "q"])
+def test_a_broken_branch_stays_alone_on_the_persistent_form(N, bad, where):
+    # node 2 is not finite: its branch is lost, the others' results do not change by a bit
+    parent = np.concatenate([[[-1, 0, 0, 1, 2, 3, -1, 6]], np.full((1, N - 8), 6)], 1).astype(np.int32)
+    cfg = config(1, N, 2, 128, BF16, [1, 1], [0, 9])
+    p = Problem(cfg, 400000, [30000], parent).to_gpu()
+    want = p.step()
+    getattr(p, "d_" + where)[0, 2, :, 5] = bad
+    o, lse = p.step()
+    clean = [n for n in range(N) if n not in (2, 4)]
+    if where == "q":
+        clean.append(4)                                    # a child shares the branch's rows, not its query
+    assert torch.equal(o[:, clean], want[0][:, clean]) and torch.equal(lse[..., clean], want[1][..., clean])
+    if where != "k":
+        assert not torch.isfinite(o[0, 2]).all(-1).any()   # in either head

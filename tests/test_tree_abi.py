@@ -271,3 +271,16 @@ def test_checks_in_python_without_the_native_part(lib, monkeypatch, module, why)
         with pytest.raises(ValueError, match="CUDA"):
             rat.rat_slot_map(cfg(B=1, T=4), None, 100, i, None, torch.zeros(1, 4, 2, dtype=torch.int64), None, ws)
     assert rat._native((), ws) is None                          # looked for once
+
+
+def test_errors_begin_with_the_argument(lib):
+    # and nothing else of its name: state_k, not state
+    full = dict(sk="state_k", sv="state_v", ck="cache_k", cv="cache_v", ok="out_state_k", ov="out_state_v")
+    for call, names in ((step, ["q", "k", "v", "g", "parent", "sk", "sv", "ck", "cv", "pos", "o", "lse"]),
+                        (commit, ["k", "v", "g", "parent", "leaf", "sk", "sv", "ok", "ov", "ck", "cv", "pos", "out_pos"])):
+        for name in names:
+            for bad in (None, P + 8):
+                if name == "lse" and bad is None:
+                    continue
+                assert call(lib, cfg(), ptrs={name: bad}) == rat.RAT_ERR_INVALID
+                assert lib.rat_last_error().decode().split()[0] == full.get(name, name)

@@ -344,7 +344,8 @@ RAT_API rat_status rat_topk_build_stats(const rat_cfg *cfg, int block, int mode,
  * One decode step with top-k block attention.  As rat_decode_step (the state
  * update, the append of the new row at row t = pos[b], ragged positions, the
  * error behaviour), plus: the new key is folded into its block's statistics,
- * which must hold blocks 0 .. c of the positions before t; `sel` (nullable,
+ * which must hold blocks 0 .. c of the positions before t (a rat_tree_commit
+ * does not keep them); `sel` (nullable,
  * device int32 [B, H, topk]) receives the selected blocks in selection order,
  * -1 where fewer were available.  ws: rat_workspace_size(cfg,
  * RAT_OP_TOPK_DECODE, cache_cap) bytes.  One kernel per step, no other CUDA
@@ -361,7 +362,10 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  * tree of candidate continuations of every sequence; one step scores all of its
  * nodes, the caller picks the branch to keep, and a commit appends it.  The
  * step of a tree that is one chain gives what as many decode steps would give,
- * and a tree step followed by a commit leaves cache and state as they do.
+ * and a tree step followed by a commit leaves cache and state as they do, but
+ * for the last bits: a step's bf16 probabilities are rounded to bf16 for the
+ * product with the values, as in a prefill (fp32 ones are not), its bf16 gates
+ * are within 2^-22, a commit's gates within two units of fp32's last place.
  *
  * Trees.  cfg->T is N, the nodes of an entry (1 <= N <= 64); token tensors are
  * [B, N, H, d].  parent is DEVICE int32 [B, N]: parent[b, i] in [0, i) is the
@@ -391,12 +395,13 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  *   cache_cap    < 2^31 - 65536
  *   o            out [B,N,H,d];  lse out [B,H,N] fp32 or NULL
  * ws: rat_workspace_size(cfg, RAT_OP_TREE, cache_cap) bytes.  Two kernels (three
- * for a large bf16 tree step with heads of one dilated set), no other CUDA call
- * after the first on a device: a step can be captured in a
- * CUDA graph and replayed with parents, positions and inputs refreshed in
- * place.  Results do not depend on the order in which the GPU runs the work; in
- * their last bits they may on the other entries' positions (where one entry's
- * rows are cut depends on how many there are in all).
+ * for a large bf16 tree step with heads of one dilated set); the host encodes
+ * TMA maps of the caches for them and asks for the current device, and makes no
+ * call that a stream capture forbids: a step can be captured in a CUDA graph and
+ * replayed with parents, positions and inputs refreshed in place.  Results do
+ * not depend on the order in which the GPU runs the work.  In their last bits
+ * they may on cache_cap, B and the other entries' positions, by which an
+ * entry's rows are cut into parts.
  */
 RAT_API rat_status rat_tree_decode_step(const rat_cfg *cfg, const void *q, const void *k, const void *v,
                                         const void *g, const int32_t *parent, const float *state_k,
@@ -418,7 +423,10 @@ RAT_API rat_status rat_tree_decode_step_paged(const rat_cfg *cfg, const void *q,
  * rows are written to the cache, out_state is the state after the leaf and
  * out_pos[b] = pos[b] + m.  parent, k, v, g, state and pos are those of the
  * tree step; out_state_k/v and out_pos may be the same memory as state_k/v and
- * pos (not otherwise overlapping).  Rows of other positions are left alone.
+ * pos (not otherwise overlapping).  Rows of other positions are left alone, and
+ * so are the block statistics of rat_topk_decode_step: before such a step,
+ * rat_topk_build_stats has to take the committed rows in (cfg->T the new length;
+ * entry by entry where lengths differ).
  * ws: rat_workspace_size(cfg, RAT_OP_STATUS, 0) bytes.  One kernel.
  */
 RAT_API rat_status rat_tree_commit(const rat_cfg *cfg, const void *k, const void *v, const void *g,
@@ -443,7 +451,9 @@ RAT_API rat_status rat_tree_commit_paged(const rat_cfg *cfg, const void *k, cons
  * 0 .. n-1 there (rat_cache_rows layout).  A page that the table names and that
  * is not needed goes back to the free stack, a needed one that it does not name
  * is taken from it, the others stay; unneeded entries become -1.  Pages are
- * given back first, then taken, both in the order of the table's entries.
+ * given back first, then taken, both in the order of the table's entries.  A
+ * page is named once, by the table or on the stack (pages that sequences share
+ * are the caller's to keep out of the call: it would give them back twice).
  *   cfg          B, H, dil, win, flags; T and the token sizes are not used
  *   page_table   in/out DEVICE int32 [B, pages_per_seq]; an entry outside
  *                [0, num_pages) names no page

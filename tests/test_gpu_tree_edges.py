@@ -168,3 +168,44 @@ def test_a_broken_branch_stays_alone_on_the_persistent_form(N, bad, where):
     assert torch.equal(o[:, clean], want[0][:, clean]) and torch.equal(lse[..., clean], want[1][..., clean])
     if where != "k":
         assert not torch.isfinite(o[0, 2]).all(-1).any()   # in either head
+
+
+def test_topk_decode_after_a_commit_and_new_statistics():
+    # the committed rows count once the block statistics hold them, entry by entry: as after as many top-k decode steps
+    d, cap, bs, K, pos, leaf = 64, 256, 8, 3, [120, 77], [10, 4]
+    cfg = config(2, 11, 2, d, BF16, [1, 1], [0, 0])
+    p = Problem(cfg, cap, pos, np.array([[i - 1 for i in range(11)]] * 2, np.int32)).to_gpu()
+    one = lambda b: cfg.replace(B=1, T=b)  # noqa: E731
+
+    def stats_of(ck, length):
+        stats = torch.zeros(rat.topk_stats_shape(cfg, bs, cap), device=DEV)
+        for b, n in enumerate(length):
+            rat.rat_topk_build_stats(one(n), bs, rat.RAT_TOPK_QUEST, ck[b:b + 1], cap, stats[b:b + 1])
+        return stats
+
+    def decode(n, x, sk, sv, ck, cv, stats, at):
+        o = torch.empty(2, 2, d, dtype=BF16, device=DEV)
+        ws = rat.workspace(cfg, rat.RAT_OP_TOPK_DECODE, cap)
+        rat.rat_topk_decode_step(cfg, bs, K, rat.RAT_TOPK_QUEST, *(y[n].contiguous() for y in x), sk, sv, ck, cv, cap, stats,
+                                 at, o, None, None, ws)
+        rat.rat_check_status(ws)
+        return o
+
+    tokens = [torch.stack([y[b, [*range(leaf[b] + 1), *[leaf[b]] * (10 - leaf[b])]] for b in range(2)], 1)
+              for y in (p.d_q, p.d_k, p.d_v, p.d_g)]          # [11, 2, H, d]: entry 1 takes its first five only
+    steps = [t.clone() for t in (p.d_sk, p.d_sv, p.ck, p.cv)] + [stats_of(p.ck, pos)]
+    for n in range(11):
+        before = [t[1:].clone() for t in steps]
+        decode(n, tokens, *steps, p.d_pos + torch.tensor([n, min(n, 5)], dtype=torch.int32, device=DEV))
+        if n > leaf[1]:
+            for t, s in zip(steps, before):
+                t[1:] = s
+    ck, cv = p.ck.clone(), p.cv.clone()
+    sk, sv, at = commit(p, leaf, ck, cv)
+    stats = stats_of(ck, at.tolist())
+    for b in range(2):
+        used = -(-int(at[b]) // bs)
+        assert torch.allclose(stats[b, :, :used], steps[4][b, :, :used], rtol=2 ** -7, atol=1e-6)
+    want = decode(3, tokens, *[t.clone() for t in steps], at)
+    got = decode(3, tokens, sk, sv, ck, cv, stats, at)
+    assert (got.float() - want.float()).abs().max() <= 2e-2

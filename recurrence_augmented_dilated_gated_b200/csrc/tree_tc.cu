@@ -82,12 +82,6 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
 __device__ __forceinline__ uint32_t idesc(int N, bool mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // two floats at once (f32x2 arithmetic: one instruction for both)
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
@@ -585,8 +579,8 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                     for (int i = 0; i < 8; i += 2) {
                         float a, c;
                         unpack2(x2[(n + i) / 2], a, c);
-                        a = ex2(a);
-                        c = ex2(c);
+                        a = exp2f_fast(a);
+                        c = exp2f_fast(c);
                         l2[(n + i) / 2] = add2(l2[(n + i) / 2], pack2(a, c));
                         __nv_bfloat162 v = __floats2bfloat162_rn(a, c);
                         pk[i / 2] = *reinterpret_cast<uint32_t *>(&v);

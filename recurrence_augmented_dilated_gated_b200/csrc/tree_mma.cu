@@ -15,9 +15,12 @@
 //   - the softmax reference of a node is raised only when a score passes it by
 //     more than 2^8 (P stays below 2^8, its sum in fp32): one vote per block of
 //     keys instead of reductions and rescaling.
-//   - bf16: m16n8k16.  P is rounded to bf16 for the product with V~ (half a
-//     step, 2^-9 of each probability; the sum of P keeps fp32): the same
-//     rounding as the prefill's.
+//   - bf16: m16n8k16.  P goes into the product with V~ in two bf16 halves (2^-15
+//     of each probability), so that what remains of the error is the output's own
+//     rounding (1.7e-3; 2.3e-3 with one bf16).  For up to 8 nodes the small halves
+//     are the free rows 8-15 of the same instruction, otherwise there is a second one:
+//     64 x 32 nodes at 16K positions, D = 16 (sets of six) 537 us with one bf16, 532 so,
+//     556 with second instructions; 4 dense heads of 17 x 33 nodes 219.6 and 221.2.
 //   - fp32: m16n8k8 on tf32 halves: x = b + s with b = x rounded to tf32 (11
 //     bits) and s = x - b, of which the instruction takes 11 bits too; x y = b b' +
 //     b s' + s b' leaves out s s' and what s was cut by, 2^-22 of the product.
@@ -65,10 +68,6 @@ template <bool kInf> __device__ __forceinline__ void split(uint32_t x, uint32_t 
     else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(b) : "f"(__uint_as_float(x)));
     small = __float_as_uint(__uint_as_float(x) - __uint_as_float(b));
     big = b;
-}
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-    __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<uint32_t *>(&t);
 }
 template <typename T> __device__ __forceinline__ bool not_finite(uint32_t w) {   // any value in a word
     if (sizeof(T) == 4) return (w & 0x7f800000u) == 0x7f800000u;
@@ -173,6 +172,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
     const int WM = padded_nodes(n_nodes) / 16, WK = kWarps / WM;
     const int wm = warp % WM, wk = warp / WM;
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;   // this lane's row (and r0 + 8) and first column of a fragment
+    const bool few = !S::kF32 && n_nodes <= 8;       // rows 8-15 hold the small halves of P
     // tiles of the parts, one part after the other
     const int end0 = n_parts > 0 ? (parts[0].n + kTile - 1) / kTile : 0;
     const int end1 = end0 + (n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0);
@@ -420,6 +420,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
                     m[u] = up ? mx[u] : m[u];
                     l[u] *= corr[u];
                 }
+                if (few) corr[1] = corr[0];
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -437,15 +438,29 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
                     }
             }
             if constexpr (!S::kF32) {
-                const uint32_t pa[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[NB - 1][0], s[NB - 1][1]),
-                                        pack2(s[NB - 1][2], s[NB - 1][3])};
+                uint32_t pa[4], pb[4];   // P: bf16 halves
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p_halves(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1], pa[i], pb[i]);
+                if (few) {
+                    pa[1] = pb[0];
+                    pa[3] = pb[2];
+                }
                 const int vr = kb * 16 + (lane & 15), vc = lane >> 4;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    uint32_t f[4];
+                for (int i = 0; i < D / 16; i += 2) {
+                    // two chunks at a time: instructions on the same sums are four apart
+                    uint32_t f[4], e[4];
                     ldsm4t(f, sv + S::at(vr, 2 * i + vc));
+                    ldsm4t(e, sv + S::at(vr, 2 * i + 2 + vc));
                     mma16816(o[2 * i], pa, f[0], f[1]);
                     mma16816(o[2 * i + 1], pa, f[2], f[3]);
+                    mma16816(o[2 * i + 2], pa, e[0], e[1]);
+                    mma16816(o[2 * i + 3], pa, e[2], e[3]);
+                    if (few) continue;
+                    mma16816(o[2 * i], pb, f[0], f[1]);
+                    mma16816(o[2 * i + 1], pb, f[2], f[3]);
+                    mma16816(o[2 * i + 2], pb, e[0], e[1]);
+                    mma16816(o[2 * i + 3], pb, e[2], e[3]);
                 }
             } else {
                 // the instruction's key index x is key 2 x, x + 4 key 2 x + 1: P's own order
@@ -471,6 +486,13 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
         }
     }
 
+    if (few) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            o[i][0] += o[i][2];
+            o[i][1] += o[i][3];
+        }
+    }
     // Join the warps that hold the same nodes: sums go to shared memory, scaled
     // to the common reference, and leave it row by row.
 #pragma unroll

@@ -6,6 +6,12 @@
 // always full however many nodes N a tree has:
 //   S^T [128 keys x N] = K~ Q^T      (A = the K~ tile, B = the nodes' queries)
 //   O^T [128 channels x N] += V~^T P^T   (A = the V~ tile read along its rows)
+// Up to 32 nodes P is in two bf16 halves side by side (p_halves; N is then 2 N, and the
+// sums are added when an item ends): what remains of the error is the output's own
+// rounding, 1.7e-3.  For 64 nodes P is one bf16 (half a step, 2^-9 of each; 2.3e-3),
+// as in the prefill: the small halves would take a slot of the ring and as many
+// instructions as the rest of the softmax, 380 us where 16 x 64 nodes take 348.  The sum
+// of P is of fp32 values in both.
 // A thread of the softmax warps owns one key (a TMEM lane) and all its scores;
 // the reference a node's scores are measured from is shared by all keys and
 // raised, for the whole CTA, only when a score passes it by more than 2^8.  The
@@ -55,6 +61,8 @@ template <int NP> struct Mem {
     static constexpr int kSlots = NP <= 32 ? 4 : kSlotsMax;
     static constexpr uint32_t kQHalf = NP * 128;
     static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
+    static constexpr bool kHalves = NP <= 32;          // P in two halves
+    static constexpr int kO = kHalves ? 2 * NP : NP;   // columns of P, and of O
 };
 constexpr int kTmemCols = 256;
 constexpr float kSlack = 8.f;            // log2 of how far P may pass 1
@@ -366,7 +374,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
         if (lane == 0) {
             int j = 0, t_all = 0, items = 0, pv_slot = -1;   // ring slots and tiles so far; slot of a V~ tile not yet multiplied
             bool pv_first = false;
-            const uint32_t iqk = idesc(NP, false), ipv = idesc(NP, true);
+            const uint32_t iqk = idesc(NP, false), ipv = idesc(Mem<NP>::kO, true);
             auto product = [&](int t) {   // O^T += V~^T P^T of tile t
                 const int s = pv_slot % kSlots;
                 if (!mbar_wait(&sh.full[s], (pv_slot / kSlots) & 1, &sh.waits) || !mbar_wait(&sh.pfull, t & 1, &sh.waits)) return false;
@@ -553,11 +561,11 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                             l2[n / 2] = pack2(a * sh.corr[n], c * sh.corr[n + 1]);
                         }
 #pragma unroll 1
-                        for (int n = 0; n < NP; n += kCols) {
+                        for (int n = 0; n < Mem<NP>::kO; n += kCols) {
                             uint32_t o[kCols];
                             ld_cols<kCols>(t_lane + 128 + n, o);
 #pragma unroll
-                            for (int i = 0; i < kCols; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.corr[n + i]);
+                            for (int i = 0; i < kCols; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.corr[n % NP + i]);
                             st_cols<kCols>(t_lane + 128 + n, o);
                         }
                     }
@@ -574,7 +582,7 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                 uint8_t *row = smem + kOffP + tid * 128;
 #pragma unroll
                 for (int n = 0; n < NP; n += 8) {
-                    uint32_t pk[4];
+                    uint32_t pk[4], ps[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         float a, c;
@@ -582,10 +590,16 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
                         a = exp2f_fast(a);
                         c = exp2f_fast(c);
                         l2[(n + i) / 2] = add2(l2[(n + i) / 2], pack2(a, c));
-                        __nv_bfloat162 v = __floats2bfloat162_rn(a, c);
-                        pk[i / 2] = *reinterpret_cast<uint32_t *>(&v);
+                        if constexpr (Mem<NP>::kHalves) {
+                            p_halves(a, c, pk[i / 2], ps[i / 2]);
+                        } else {
+                            __nv_bfloat162 v = __floats2bfloat162_rn(a, c);
+                            pk[i / 2] = *reinterpret_cast<uint32_t *>(&v);
+                        }
                     }
                     *reinterpret_cast<uint4 *>(row + (((n >> 3) ^ (tid & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    if constexpr (Mem<NP>::kHalves)
+                        *reinterpret_cast<uint4 *>(row + (((NP + n >> 3) ^ (tid & 7)) << 4)) = make_uint4(ps[0], ps[1], ps[2], ps[3]);
                 }
                 if (tail) {
                     // rows behind the item's last hold anything: their values are
@@ -639,11 +653,12 @@ tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
             tc_after();
 #pragma unroll 1
             for (int n = 0; n < NP; n += kCols) {
-                uint32_t o[kCols];
+                uint32_t o[kCols], e[kCols] = {};
                 ld_cols<kCols>(t_lane + 128 + n, o);
+                if constexpr (Mem<NP>::kHalves) ld_cols<kCols>(t_lane + 128 + NP + n, e);
 #pragma unroll
                 for (int i = 0; i < kCols; ++i)
-                    if (n + i < p.N) p.part[(rowbase + n + i) * kD + tid] = __uint_as_float(o[i]);
+                    if (n + i < p.N) p.part[(rowbase + n + i) * kD + tid] = __uint_as_float(o[i]) + __uint_as_float(e[i]);
             }
             tc_before();
             softmax_sync();   // sh.nref and sh.part are read

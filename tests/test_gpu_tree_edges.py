@@ -209,3 +209,23 @@ def test_topk_decode_after_a_commit_and_new_statistics():
     want = decode(3, tokens, *[t.clone() for t in steps], at)
     got = decode(3, tokens, sk, sv, ck, cv, stats, at)
     assert (got.float() - want.float()).abs().max() <= 2e-2
+
+
+@pytest.mark.parametrize("cap", [60, 800000])               # 800000 rows: the persistent form where d = 128
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [4, 20, 40])                   # of up to 32 nodes, or the register-fragment one
+def test_bf16_outputs_are_as_exact_as_their_type(cap, d, N):
+    # Few keys with probabilities of all sizes, rows that are the tokens (no recurrence).  The output's own rounding is
+    # at most half a step, eps / 2 = 2^-8 of the value.  The rest: probabilities within 2^-15, so their part of the sum
+    # within 2^-15 max|v|; scores of d products in fp32, each within 2^-24 sum|q k| (1 + d), under 2^-24 * 129 * 3 * d^0.5
+    # here after scaling (|q k| averages 2 / pi, its scaled sum stays below 3 d^0.5), 2^-12.4 at worst and a
+    # sixteenth of it, 2^-16, for sums that are rounded to nearest at random: 2^-13 max|v| holds all of it.
+    if N > 32 and d == 128:
+        cap = min(cap, 90000)                                # there P is one bf16: below its threshold
+    cfg = config(2, N, 1, d, BF16, [1], [0], [0])
+    parent = np.full((2, N), -1, np.int32)
+    p = Problem(cfg, cap, [6, 17], parent, std=1.0).to_gpu()
+    o, _ = p.step()
+    ro, _ = p.reference()
+    err, top = np.abs(f64(o) - ro), max(f64(p.hv).max(), f64(p.v).max(), -f64(p.hv).min(), -f64(p.v).min())
+    assert (err <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -13 * top).all(), (err - 2.0 ** -8 * np.abs(ro)).max() / top

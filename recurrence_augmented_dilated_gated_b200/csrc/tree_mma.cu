@@ -20,7 +20,9 @@
 //     rounding (1.7e-3; 2.3e-3 with one bf16).  For up to 8 nodes the small halves
 //     are the free rows 8-15 of the same instruction, otherwise there is a second one:
 //     64 x 32 nodes at 16K positions, D = 16 (sets of six) 537 us with one bf16, 532 so,
-//     556 with second instructions; 4 dense heads of 17 x 33 nodes 219.6 and 221.2.
+//     556 with second instructions.  Those cost most where many nodes read the same rows
+//     and tree_tc.cu does not take them: 9 x 38 nodes, 28 dense heads of 4012 rows, d = 64
+//     142 us with one bf16, 160 so; the mean of 60 drawn steps is 1 % longer.
 //   - fp32: m16n8k8 on tf32 halves: x = b + s with b = x rounded to tf32 (11
 //     bits) and s = x - b, of which the instruction takes 11 bits too; x y = b b' +
 //     b s' + s b' leaves out s s' and what s was cut by, 2^-22 of the product.

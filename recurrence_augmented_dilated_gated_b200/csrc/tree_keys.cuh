@@ -114,14 +114,16 @@ __device__ __forceinline__ float exp2f_fast(float x) {
     return y;
 }
 // Two probabilities as bf16 halves, for products with bf16 values: x cut to bf16, and
-// what that leaves, rounded (2^-9 of it, 2^-17 of x) with its last bit set (2^-15 of x
-// at most).  Both halves of a probability are then above 0, so that an infinite value
-// comes out with its sign; one rounded bf16 alone (2^-9) would be most of the step's error.
+// what that leaves, rounded (2^-9 of it, 2^-17 of x).  The last bit of x is set first
+// (2^-23), so that both halves of a probability are above 0 and an infinite value comes
+// out with its sign; a probability of 0 has halves of 0 (2^-149 rounds to it).  One
+// rounded bf16 alone, 2^-9, would be most of the step's error.
 __device__ __forceinline__ void p_halves(float x, float y, uint32_t &big, uint32_t &small) {
-    const uint32_t xi = __float_as_uint(x), yi = __float_as_uint(y);
+    const uint32_t xi = __float_as_uint(x) | 1u, yi = __float_as_uint(y) | 1u;
     big = __byte_perm(xi, yi, 0x7632);
-    const __nv_bfloat162 t = __floats2bfloat162_rn(x - __uint_as_float(xi & 0xffff0000u), y - __uint_as_float(yi & 0xffff0000u));
-    small = *reinterpret_cast<const uint32_t *>(&t) | 0x00010001u;
+    const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(xi) - __uint_as_float(xi & 0xffff0000u),
+                                                   __uint_as_float(yi) - __uint_as_float(yi & 0xffff0000u));
+    small = *reinterpret_cast<const uint32_t *>(&t);
 }
 
 // The gate for a state that is rounded to T.  For bf16 rows the exponential is the

@@ -15,14 +15,15 @@
 //   - the softmax reference of a node is raised only when a score passes it by
 //     more than 2^8 (P stays below 2^8, its sum in fp32): one vote per block of
 //     keys instead of reductions and rescaling.
-//   - bf16: m16n8k16.  P goes into the product with V~ in two bf16 halves (2^-15
-//     of each probability), so that what remains of the error is the output's own
-//     rounding (1.7e-3; 2.3e-3 with one bf16).  For up to 8 nodes the small halves
-//     are the free rows 8-15 of the same instruction, otherwise there is a second one:
-//     64 x 32 nodes at 16K positions, D = 16 (sets of six) 537 us with one bf16, 532 so,
-//     556 with second instructions.  Those cost most where many nodes read the same rows
-//     and tree_tc.cu does not take them: 9 x 38 nodes, 28 dense heads of 4012 rows, d = 64
-//     142 us with one bf16, 160 so; the mean of 60 drawn steps is 1 % longer.
+//   - bf16: m16n8k16.  An item of up to 8 nodes has P for the product with V~ in two
+//     bf16 halves (2^-17 of each probability), the small ones in the free rows 8-15 of
+//     the same instruction: what remains of the error is the output's own rounding,
+//     1.7e-3 (64 x 32 nodes at 16K positions, D = 16, sets of six: 537 us with one bf16,
+//     531 so).  Items of 9 to 16 nodes take a second instruction where the tree has no
+//     more (kTwice).  With more nodes on the same rows the instructions are the time,
+//     and P is one bf16 there (half a step, 2^-9; error 2.3e-3), as in the prefill: 24
+//     and 48 nodes of 4 x 16 heads over 16000 rows 134 and 209 us, with second
+//     instructions 142 and 240.  The sum of P is of fp32 values in all of them.
 //   - fp32: m16n8k8 on tf32 halves: x = b + s with b = x rounded to tf32 (11
 //     bits) and s = x - b, of which the instruction takes 11 bits too; x y = b b' +
 //     b s' + s b' leaves out s s' and what s was cut by, 2^-22 of the product.
@@ -70,6 +71,10 @@ template <bool kInf> __device__ __forceinline__ void split(uint32_t x, uint32_t 
     else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(b) : "f"(__uint_as_float(x)));
     small = __float_as_uint(__uint_as_float(x) - __uint_as_float(b));
     big = b;
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<uint32_t *>(&t);
 }
 template <typename T> __device__ __forceinline__ bool not_finite(uint32_t w) {   // any value in a word
     if (sizeof(T) == 4) return (w & 0x7f800000u) == 0x7f800000u;
@@ -162,7 +167,7 @@ __device__ __noinline__ void count_keys(Shared &sh, int n_nodes, int k0, bool no
 // is and which tiles carry a mask): a second copy of it would only thrash the
 // instruction cache.
 enum ItemEnd { kDone, kGaveUp, kAgain };   // a wait gave up; nothing written, to be taken again with kInf
-template <typename T, int D, bool kInf>
+template <typename T, int D, bool kTwice, bool kInf>
 __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &maps, Shared &sh, uint8_t *ring, const Keys *parts,
                                          int n_parts, int b, int h, int pos, int slot, int &fills) {
     using S = Shape<T, D>;
@@ -446,6 +451,9 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
                 if (few) {
                     pa[1] = pb[0];
                     pa[3] = pb[2];
+                } else if (!kTwice) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pa[i] = pack2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
                 }
                 const int vr = kb * 16 + (lane & 15), vc = lane >> 4;
 #pragma unroll
@@ -458,7 +466,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
                     mma16816(o[2 * i + 1], pa, f[2], f[3]);
                     mma16816(o[2 * i + 2], pa, e[0], e[1]);
                     mma16816(o[2 * i + 3], pa, e[2], e[3]);
-                    if (few) continue;
+                    if (!kTwice || few) continue;
                     mma16816(o[2 * i], pb, f[0], f[1]);
                     mma16816(o[2 * i + 1], pb, f[2], f[3]);
                     mma16816(o[2 * i + 2], pb, e[0], e[1]);
@@ -606,7 +614,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
     return kDone;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kTwice>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -660,9 +668,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
             __syncthreads();
             if (tid < 32) list_nodes(p, sh.ti, h, x % sets, sh.nodes, &sh.n);
         }
-        ItemEnd end = run_item<T, D, false>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
+        ItemEnd end = run_item<T, D, kTwice, false>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
         if constexpr (sizeof(T) == 4) {
-            if (end == kAgain) end = run_item<T, D, true>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
+            if (end == kAgain) end = run_item<T, D, kTwice, true>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
         }
         if (end == kGaveUp) break;
     }
@@ -671,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
     if (blockIdx.x == gridDim.x - 1) wait_previous();
 }
 
-template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
+template <typename T, int D, bool kTwice> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
     using S = Shape<T, D>;
     static_assert(S::kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
     static_assert(S::kTile <= kTileMax && S::kStages <= kStagesMax, "tile and ring as declared");
@@ -680,22 +688,22 @@ template <typename T, int D> cudaError_t launch_typed(const TreeParams &p, unsig
     static std::atomic<unsigned long long> smem_set{0};
     // the limit is raised once per device, so to the largest tree's
     const size_t most = S::kRing + (S::kF32 ? q_bytes<D>(kTreeMaxNodes) : 0), most_tree = TreeWalk<T, D>::bytes(kTreeMaxNodes, 1);
-    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D>, (most > most_tree ? most : most_tree) + 1024, smem_set, true);
+    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D, kTwice>, (most > most_tree ? most : most_tree) + 1024, smem_set, true);
     if (e != cudaSuccess) return e;
     Maps maps = {};
     if (!p.page_table)
         for (int x = 0; x < 2; ++x)
             if (!encode_map_rows(&maps.kv[x], p.cache[x], sizeof(T) == 4 ? RAT_F32 : RAT_BF16, p.cache_R, (long long)p.B * p.H, D, S::kTile))
                 return cudaErrorInvalidValue;
-    return launch_after(tree_mma_kernel<T, D>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
+    return launch_after(tree_mma_kernel<T, D, kTwice>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_mma(const TreeParams &p, int dtype, unsigned grid, cudaStream_t s) {
-    if (dtype == RAT_BF16)
-        return p.d == 128 ? launch_typed<__nv_bfloat16, 128>(p, grid, s) : launch_typed<__nv_bfloat16, 64>(p, grid, s);
-    return p.d == 128 ? launch_typed<float, 128>(p, grid, s) : launch_typed<float, 64>(p, grid, s);
+    if (dtype == RAT_F32) return p.d == 128 ? launch_typed<float, 128, false>(p, grid, s) : launch_typed<float, 64, false>(p, grid, s);
+    if (p.N <= 16) return p.d == 128 ? launch_typed<__nv_bfloat16, 128, true>(p, grid, s) : launch_typed<__nv_bfloat16, 64, true>(p, grid, s);
+    return p.d == 128 ? launch_typed<__nv_bfloat16, 128, false>(p, grid, s) : launch_typed<__nv_bfloat16, 64, false>(p, grid, s);
 }
 
 }  // namespace rat

@@ -6,12 +6,13 @@
 // always full however many nodes N a tree has:
 //   S^T [128 keys x N] = K~ Q^T      (A = the K~ tile, B = the nodes' queries)
 //   O^T [128 channels x N] += V~^T P^T   (A = the V~ tile read along its rows)
-// Up to 32 nodes P is in two bf16 halves side by side (p_halves; N is then 2 N, and the
+// Up to 16 nodes P is in two bf16 halves side by side (p_halves; N is then 2 N, and the
 // sums are added when an item ends): what remains of the error is the output's own
-// rounding, 1.7e-3.  For 64 nodes P is one bf16 (half a step, 2^-9 of each; 2.3e-3),
-// as in the prefill: the small halves would take a slot of the ring and as many
-// instructions as the rest of the softmax, 380 us where 16 x 64 nodes take 348.  The sum
-// of P is of fp32 values in both.
+// rounding, 1.7e-3 (4 x 8 nodes, 16 heads over 16000 rows 97 us either way).  For more, P
+// is one bf16 (half a step, 2^-9 of each; 2.3e-3), as in the prefill: the small halves
+// are as many instructions as the rest of the softmax, and for 64 nodes a slot of the
+// ring (4 x 24 nodes 104 us, 121 with them; 16 x 64 nodes 348 and 380).  The sum of P
+// is of fp32 values in all.
 // A thread of the softmax warps owns one key (a TMEM lane) and all its scores;
 // the reference a node's scores are measured from is shared by all keys and
 // raised, for the whole CTA, only when a score passes it by more than 2^8.  The
@@ -61,7 +62,7 @@ template <int NP> struct Mem {
     static constexpr int kSlots = NP <= 32 ? 4 : kSlotsMax;
     static constexpr uint32_t kQHalf = NP * 128;
     static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
-    static constexpr bool kHalves = NP <= 32;          // P in two halves
+    static constexpr bool kHalves = NP <= 16;          // P in two halves
     static constexpr int kO = kHalves ? 2 * NP : NP;   // columns of P, and of O
 };
 constexpr int kTmemCols = 256;

@@ -213,19 +213,40 @@ def test_topk_decode_after_a_commit_and_new_statistics():
 
 @pytest.mark.parametrize("cap", [60, 800000])               # 800000 rows: the persistent form where d = 128
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("N", [4, 20, 40])                   # of up to 32 nodes, or the register-fragment one
-def test_bf16_outputs_are_as_exact_as_their_type(cap, d, N):
-    # Few keys with probabilities of all sizes, rows that are the tokens (no recurrence).  The output's own rounding is
-    # at most half a step, eps / 2 = 2^-8 of the value.  The rest: probabilities within 2^-15, so their part of the sum
-    # within 2^-15 max|v|; scores of d products in fp32, each within 2^-24 sum|q k| (1 + d), under 2^-24 * 129 * 3 * d^0.5
-    # here after scaling (|q k| averages 2 / pi, its scaled sum stays below 3 d^0.5), 2^-12.4 at worst and a
-    # sixteenth of it, 2^-16, for sums that are rounded to nearest at random: 2^-13 max|v| holds all of it.
-    if N > 32 and d == 128:
-        cap = min(cap, 90000)                                # there P is one bf16: below its threshold
-    cfg = config(2, N, 1, d, BF16, [1], [0], [0])
-    parent = np.full((2, N), -1, np.int32)
-    p = Problem(cfg, cap, [6, 17], parent, std=1.0).to_gpu()
+@pytest.mark.parametrize("N,D", [(1, 1), (4, 1), (8, 1), (9, 1), (16, 1), (40, 8)])
+def test_bf16_outputs_are_as_exact_as_their_type(cap, d, N, D):
+    # Few keys with probabilities of all sizes, rows that are the tokens (no recurrence), up to 16 nodes on the same rows
+    # (N = 40: held rows by sets of at most five; the nodes, one item for all, are given no weight).  The output's own
+    # rounding is at most half a step, eps / 2 = 2^-8 of the value.  The rest: probabilities within 2^-17, so their part
+    # of the sum within 2^-17 max|v|; scores of d products in fp32, each within 2^-24 sum|q k| (1 + d), under
+    # 2^-24 * 129 * 3 * d^0.5 here after scaling (|q k| averages 2 / pi, its scaled sum stays below 3 d^0.5), 2^-12.4 at
+    # worst and a sixteenth of it, 2^-16, for sums that are rounded to nearest at random: 2^-13 max|v| holds all of it.
+    cfg = config(2, N, 1, d, BF16, [D], [0], [0])
+    parent = np.full((2, N), -1, np.int32) if D == 1 else np.array([[i - 5 if i >= 5 else -1 for i in range(N)]] * 2, np.int32)
+    p = Problem(cfg, cap, [6, 17] if D == 1 else [43, 120 if cap > 200 else 52], parent, std=1.0)
+    if D > 1:
+        p.q[..., 0], p.k[..., 0] = 8.0, -100.0
+    p.to_gpu()
     o, _ = p.step()
     ro, _ = p.reference()
     err, top = np.abs(f64(o) - ro), max(f64(p.hv).max(), f64(p.v).max(), -f64(p.hv).min(), -f64(p.v).min())
     assert (err <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -13 * top).all(), (err - 2.0 ** -8 * np.abs(ro)).max() / top
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("D,W,N", [(1, 0, 6), (1, 0, 20), (1, 9, 40), (3, 5, 12)])
+def test_a_key_left_out_leaves_nothing_behind(dtype, d, D, W, N):
+    # a weight of 0 is 0: the largest finite values in a branch, or in a held row whose score is -inf, do not reach the
+    # nodes that do not see them, by a bit
+    parent = np.concatenate([[[-1, 0, 0, -1, 3, 4]], np.full((1, N - 6), 3)], 1).astype(np.int32)
+    cfg = config(1, N, 1, d, dtype, [D], [W])
+    p = Problem(cfg, 200, [130], parent)
+    p.q[..., 5] = p.q[..., 5].abs() + 0.5
+    p.hk[0, 100, 0, 5] = -float("inf")
+    p.to_gpu()
+    want = p.step()
+    p.d_v[0, :3] = torch.finfo(dtype).max                  # nodes 0 to 2; the others hang below node 3
+    p.cv[0, 0, [(100 % D) * -(-200 // D) + 100 // D]] = -torch.finfo(dtype).max
+    o, lse = p.step()
+    assert torch.equal(o[:, 3:], want[0][:, 3:]) and torch.equal(lse[..., 3:], want[1][..., 3:])

@@ -250,3 +250,15 @@ def test_a_key_left_out_leaves_nothing_behind(dtype, d, D, W, N):
     p.cv[0, 0, [(100 % D) * -(-200 // D) + 100 // D]] = -torch.finfo(dtype).max
     o, lse = p.step()
     assert torch.equal(o[:, 3:], want[0][:, 3:]) and torch.equal(lse[..., 3:], want[1][..., 3:])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_fewer_pieces_than_the_capacity_has_runs(dtype):
+    # 544 pairs: a dense head's rows are cut into at most 27 pieces, a long window likewise, whatever the capacity
+    rng = np.random.default_rng(13)
+    B, H, N, cap = 17, 32, 5, 7200
+    cfg = config(B, N, H, 64, dtype, [1] * 4 + [48] * 28, [0, 6000, 0, 0] + [37] * 28, [0] * 4 + [1] * 28)
+    pos = [int(x) for x in rng.integers(0, 90, B)]
+    pos[5] = 7100
+    p = Problem(cfg, cap, pos, random_parents(rng, B, N, 3)).to_gpu()
+    p.check(*p.step())

@@ -364,8 +364,9 @@ RAT_API rat_status rat_topk_decode_step(const rat_cfg *cfg, int block, int topk,
  * step of a tree that is one chain gives what as many decode steps would give,
  * and a tree step followed by a commit leaves cache and state as they do, but
  * for the last bits: a bf16 step's probabilities are within 2^-17 (2^-9, as in a
- * prefill, where more than 16 nodes read the same rows) and its gates within
- * 2^-22, a commit's gates within two units of fp32's last place.
+ * prefill, for d = 64 and more than 16 nodes and, over many rows that all nodes
+ * read, for more than 32) and its gates within 2^-22, a commit's gates within two
+ * units of fp32's last place.
  *
  * Trees.  cfg->T is N, the nodes of an entry (1 <= N <= 64); token tensors are
  * [B, N, H, d].  parent is DEVICE int32 [B, N]: parent[b, i] in [0, i) is the

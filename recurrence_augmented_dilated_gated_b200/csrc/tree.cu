@@ -172,9 +172,10 @@ TreeLayout tree_plan(const rat_cfg *c, int cap, int page_rows, TreeParams *p) {
     constexpr int kSetsGuess = 8, kSMs = 148;
     // tree_tc.cu takes heads whose nodes all read the same rows, from this many held
     // rows on (by capacity, with caches held to it).  Both forms measured warm, 16 heads, 8 / 24 / 48 nodes:
-    // 1 x 16000 positions (0.24 M rows) tree_tc 43 / 50 / 82 us, tree_mma 38 / 47 / 69;
-    // 4 x 8000 (0.49 M) 61 / 67 / 94 against 63 / 82 / 126; 4 x 16000 (0.98 M) 97 / 105 /
-    // 128 against 107 / 134 / 209; 8 x 16000 (1.95 M) 172 / 178 / 198 against 194 / 235 / 369.
+    // 1 x 16000 positions (0.24 M rows) tree_tc 43 / 50 / 82 us, tree_mma 38 / 51 / 78;
+    // 4 x 8000 (0.49 M) 61 / 69 / 94 against 63 / 87 / 138; 4 x 16000 (0.98 M) 97 / 107 /
+    // 127 against 107 / 142 / 240; 8 x 16000 (1.95 M) 172 / 180 / 198 against 194 / 250 / 414.
+    // (6 x 20 nodes, 28 grid heads with W = 128, 0.63 M rows: 100 against 91.)
     const long long kTcMinRows = c->T > 32 ? 3 << 17 : 3 << 18;
     const bool grid = (c->flags & RAT_FLAG_GRID_DILATION) != 0;
     const int N = c->T;

@@ -15,15 +15,15 @@
 //   - the softmax reference of a node is raised only when a score passes it by
 //     more than 2^8 (P stays below 2^8, its sum in fp32): one vote per block of
 //     keys instead of reductions and rescaling.
-//   - bf16: m16n8k16.  An item of up to 8 nodes has P for the product with V~ in two
-//     bf16 halves (2^-17 of each probability), the small ones in the free rows 8-15 of
-//     the same instruction: what remains of the error is the output's own rounding,
-//     1.7e-3 (64 x 32 nodes at 16K positions, D = 16, sets of six: 537 us with one bf16,
-//     531 so).  Items of 9 to 16 nodes take a second instruction where the tree has no
-//     more (kTwice).  With more nodes on the same rows the instructions are the time,
-//     and P is one bf16 there (half a step, 2^-9; error 2.3e-3), as in the prefill: 24
-//     and 48 nodes of 4 x 16 heads over 16000 rows 134 and 209 us, with second
-//     instructions 142 and 240.  The sum of P is of fp32 values in all of them.
+//   - bf16: m16n8k16.  P goes into the product with V~ in two bf16 halves (2^-17 of
+//     each probability; kHalves), so that what remains of the error is the output's
+//     own rounding, 1.7e-3.  An item of up to 8 nodes has the small ones in the free
+//     rows 8-15 of the same instruction (64 x 32 nodes at 16K positions, D = 16, sets of
+//     six: 537 us with one bf16, 531 so); with more nodes there is a second one.  For
+//     d = 64 and more than 16 nodes the instructions are the time and P is one bf16
+//     (half a step, 2^-9; error 2.3e-3), as in the prefill: 9 x 38 nodes, 28 dense heads
+//     of 4012 rows 142 us, with second instructions 163 (d = 128 at 0.24 M rows, 48 nodes,
+//     the most that tree_tc.cu leaves: 69 and 77).  The sum of P is of fp32 values.
 //   - fp32: m16n8k8 on tf32 halves: x = b + s with b = x rounded to tf32 (11
 //     bits) and s = x - b, of which the instruction takes 11 bits too; x y = b b' +
 //     b s' + s b' leaves out s s' and what s was cut by, 2^-22 of the product.
@@ -167,7 +167,7 @@ __device__ __noinline__ void count_keys(Shared &sh, int n_nodes, int k0, bool no
 // is and which tiles carry a mask): a second copy of it would only thrash the
 // instruction cache.
 enum ItemEnd { kDone, kGaveUp, kAgain };   // a wait gave up; nothing written, to be taken again with kInf
-template <typename T, int D, bool kTwice, bool kInf>
+template <typename T, int D, bool kHalves, bool kInf>
 __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &maps, Shared &sh, uint8_t *ring, const Keys *parts,
                                          int n_parts, int b, int h, int pos, int slot, int &fills) {
     using S = Shape<T, D>;
@@ -179,7 +179,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
     const int WM = padded_nodes(n_nodes) / 16, WK = kWarps / WM;
     const int wm = warp % WM, wk = warp / WM;
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;   // this lane's row (and r0 + 8) and first column of a fragment
-    const bool few = !S::kF32 && n_nodes <= 8;       // rows 8-15 hold the small halves of P
+    const bool few = kHalves && n_nodes <= 8;        // rows 8-15 hold the small halves of P
     // tiles of the parts, one part after the other
     const int end0 = n_parts > 0 ? (parts[0].n + kTile - 1) / kTile : 0;
     const int end1 = end0 + (n_parts > 1 ? (parts[1].n + kTile - 1) / kTile : 0);
@@ -445,15 +445,16 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
                     }
             }
             if constexpr (!S::kF32) {
-                uint32_t pa[4], pb[4];   // P: bf16 halves
+                uint32_t pa[4], pb[4];   // P: bf16 halves, or one bf16
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p_halves(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1], pa[i], pb[i]);
+                for (int i = 0; i < 4; ++i) {
+                    const float x = s[i >> 1][2 * (i & 1)], y = s[i >> 1][2 * (i & 1) + 1];
+                    if (kHalves) p_halves(x, y, pa[i], pb[i]);
+                    else pa[i] = pack2(x, y);
+                }
                 if (few) {
                     pa[1] = pb[0];
                     pa[3] = pb[2];
-                } else if (!kTwice) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) pa[i] = pack2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
                 }
                 const int vr = kb * 16 + (lane & 15), vc = lane >> 4;
 #pragma unroll
@@ -466,7 +467,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
                     mma16816(o[2 * i + 1], pa, f[2], f[3]);
                     mma16816(o[2 * i + 2], pa, e[0], e[1]);
                     mma16816(o[2 * i + 3], pa, e[2], e[3]);
-                    if (!kTwice || few) continue;
+                    if (!kHalves || few) continue;
                     mma16816(o[2 * i], pb, f[0], f[1]);
                     mma16816(o[2 * i + 1], pb, f[2], f[3]);
                     mma16816(o[2 * i + 2], pb, e[0], e[1]);
@@ -614,7 +615,7 @@ __device__ __forceinline__ ItemEnd run_item(const TreeParams &p, const Maps &map
     return kDone;
 }
 
-template <typename T, int D, bool kTwice>
+template <typename T, int D, bool kHalves>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -668,9 +669,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
             __syncthreads();
             if (tid < 32) list_nodes(p, sh.ti, h, x % sets, sh.nodes, &sh.n);
         }
-        ItemEnd end = run_item<T, D, kTwice, false>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
+        ItemEnd end = run_item<T, D, kHalves, false>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
         if constexpr (sizeof(T) == 4) {
-            if (end == kAgain) end = run_item<T, D, kTwice, true>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
+            if (end == kAgain) end = run_item<T, D, kHalves, true>(p, maps, sh, ring, parts, n, b, h, pos, slot, fills);
         }
         if (end == kGaveUp) break;
     }
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) tree_mma_ker
     if (blockIdx.x == gridDim.x - 1) wait_previous();
 }
 
-template <typename T, int D, bool kTwice> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
+template <typename T, int D, bool kHalves> cudaError_t launch_typed(const TreeParams &p, unsigned grid, cudaStream_t s) {
     using S = Shape<T, D>;
     static_assert(S::kRing >= kWarps * 16 * D * sizeof(float), "the warps' sums fit");
     static_assert(S::kTile <= kTileMax && S::kStages <= kStagesMax, "tile and ring as declared");
@@ -688,22 +689,22 @@ template <typename T, int D, bool kTwice> cudaError_t launch_typed(const TreePar
     static std::atomic<unsigned long long> smem_set{0};
     // the limit is raised once per device, so to the largest tree's
     const size_t most = S::kRing + (S::kF32 ? q_bytes<D>(kTreeMaxNodes) : 0), most_tree = TreeWalk<T, D>::bytes(kTreeMaxNodes, 1);
-    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D, kTwice>, (most > most_tree ? most : most_tree) + 1024, smem_set, true);
+    cudaError_t e = ensure_smem_limit(tree_mma_kernel<T, D, kHalves>, (most > most_tree ? most : most_tree) + 1024, smem_set, true);
     if (e != cudaSuccess) return e;
     Maps maps = {};
     if (!p.page_table)
         for (int x = 0; x < 2; ++x)
             if (!encode_map_rows(&maps.kv[x], p.cache[x], sizeof(T) == 4 ? RAT_F32 : RAT_BF16, p.cache_R, (long long)p.B * p.H, D, S::kTile))
                 return cudaErrorInvalidValue;
-    return launch_after(tree_mma_kernel<T, D, kTwice>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
+    return launch_after(tree_mma_kernel<T, D, kHalves>, grid, kThreads, smem, s, p.n_tc > 0, p, maps);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_mma(const TreeParams &p, int dtype, unsigned grid, cudaStream_t s) {
     if (dtype == RAT_F32) return p.d == 128 ? launch_typed<float, 128, false>(p, grid, s) : launch_typed<float, 64, false>(p, grid, s);
-    if (p.N <= 16) return p.d == 128 ? launch_typed<__nv_bfloat16, 128, true>(p, grid, s) : launch_typed<__nv_bfloat16, 64, true>(p, grid, s);
-    return p.d == 128 ? launch_typed<__nv_bfloat16, 128, false>(p, grid, s) : launch_typed<__nv_bfloat16, 64, false>(p, grid, s);
+    if (p.d == 128) return launch_typed<__nv_bfloat16, 128, true>(p, grid, s);
+    return p.N <= 16 ? launch_typed<__nv_bfloat16, 64, true>(p, grid, s) : launch_typed<__nv_bfloat16, 64, false>(p, grid, s);
 }
 
 }  // namespace rat

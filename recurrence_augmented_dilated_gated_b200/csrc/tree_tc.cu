@@ -6,13 +6,12 @@
 // always full however many nodes N a tree has:
 //   S^T [128 keys x N] = K~ Q^T      (A = the K~ tile, B = the nodes' queries)
 //   O^T [128 channels x N] += V~^T P^T   (A = the V~ tile read along its rows)
-// Up to 16 nodes P is in two bf16 halves side by side (p_halves; N is then 2 N, and the
+// Up to 32 nodes P is in two bf16 halves side by side (p_halves; N is then 2 N, and the
 // sums are added when an item ends): what remains of the error is the output's own
-// rounding, 1.7e-3 (4 x 8 nodes, 16 heads over 16000 rows 97 us either way).  For more, P
-// is one bf16 (half a step, 2^-9 of each; 2.3e-3), as in the prefill: the small halves
-// are as many instructions as the rest of the softmax, and for 64 nodes a slot of the
-// ring (4 x 24 nodes 104 us, 121 with them; 16 x 64 nodes 348 and 380).  The sum of P
-// is of fp32 values in all.
+// rounding, 1.7e-3 (4 x 24 nodes, 16 heads over 16000 rows 105 us, 106 with them).  For
+// more, P is one bf16 (half a step, 2^-9 of each; 2.3e-3), as in the prefill: the small
+// halves would take a slot of the ring and twice the softmax's instructions (16 x 64
+// nodes 348 and 380).  The sum of P is of fp32 values in both.
 // A thread of the softmax warps owns one key (a TMEM lane) and all its scores;
 // the reference a node's scores are measured from is shared by all keys and
 // raised, for the whole CTA, only when a score passes it by more than 2^8.  The
@@ -56,13 +55,15 @@ constexpr uint32_t kHalf = kTile * 128;  // 64 channels of a tile: rows of 128 b
 constexpr uint32_t kSlot = 2 * kHalf;    // a K~ or a V~ tile
 // Four slots for up to 32 nodes: beside them an SM has room for a CTA of
 // tree_mma.cu (64 KB), which then does the windows and the nodes while this kernel
-// streams (32 x 16 nodes on a paged grid 136 -> 121 us).  For 64 nodes Q leaves it no room, and six slots
+// streams (32 x 16 nodes on a paged grid 136 -> 121 us).  That takes no more than 168 registers a
+// thread too, with which two of this kernel's warps and one of tree_mma.cu's fit in a quarter
+// of the SM (4 x 24 nodes, 16 heads over 16000 rows 104 us, with 170 registers 119).  For 64 nodes Q leaves it no room, and six slots
 // are 2 % faster than four.
 template <int NP> struct Mem {
     static constexpr int kSlots = NP <= 32 ? 4 : kSlotsMax;
     static constexpr uint32_t kQHalf = NP * 128;
     static constexpr uint32_t kOffQ = kSlots * kSlot, kOffP = kOffQ + 2 * kQHalf, kBytes = kOffP + kTile * 128;
-    static constexpr bool kHalves = NP <= 16;          // P in two halves
+    static constexpr bool kHalves = NP <= 32;          // P in two halves
     static constexpr int kO = kHalves ? 2 * NP : NP;   // columns of P, and of O
 };
 constexpr int kTmemCols = 256;
@@ -328,7 +329,7 @@ struct Maps {
 };
 
 template <int NP>   // nodes, padded to 16, 32 or 64
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, NP <= 32 ? 2 : 1)   // 168 registers: see Mem
 tree_tc_kernel(const TreeParams p, const __grid_constant__ Maps maps) {
     constexpr int kSlots = Mem<NP>::kSlots;
     constexpr uint32_t kQHalf = Mem<NP>::kQHalf, kOffQ = Mem<NP>::kOffQ, kOffP = Mem<NP>::kOffP;

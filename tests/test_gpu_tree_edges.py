@@ -211,21 +211,20 @@ def test_topk_decode_after_a_commit_and_new_statistics():
     assert (got.float() - want.float()).abs().max() <= 2e-2
 
 
-@pytest.mark.parametrize("cap", [60, 800000])               # 800000 rows: the persistent form where d = 128
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("N,D", [(1, 1), (4, 1), (8, 1), (9, 1), (16, 1), (40, 8)])
+@pytest.mark.parametrize("cap,d,N,D", [                     # 800000 rows: the persistent form where d = 128
+    *((cap, d, N, 1) for cap in (60, 800000) for d in (64, 128) for N in (1, 4, 8, 9, 16)),
+    *((cap, 128, N, 1) for cap, N in ((60, 20), (60, 33), (60, 64), (800000, 17), (800000, 32), (150000, 40))),
+    (60, 128, 40, 8), (800000, 128, 40, 8)])
 def test_bf16_outputs_are_as_exact_as_their_type(cap, d, N, D):
-    # Few keys with probabilities of all sizes, rows that are the tokens (no recurrence), up to 16 nodes on the same rows
-    # (N = 40: held rows by sets of at most five; the nodes, one item for all, are given no weight).  The output's own
-    # rounding is at most half a step, eps / 2 = 2^-8 of the value.  The rest: probabilities within 2^-17, so their part
-    # of the sum within 2^-17 max|v|; scores of d products in fp32, each within 2^-24 sum|q k| (1 + d), under
-    # 2^-24 * 129 * 3 * d^0.5 here after scaling (|q k| averages 2 / pi, its scaled sum stays below 3 d^0.5), 2^-12.4 at
-    # worst and a sixteenth of it, 2^-16, for sums that are rounded to nearest at random: 2^-13 max|v| holds all of it.
+    # Few keys with probabilities of all sizes, rows that are the tokens (no recurrence); D = 8: held rows by sets of five
+    # nodes.  The output's own rounding is at most half a step, eps / 2 = 2^-8 of the value.  The rest: probabilities
+    # within 2^-17, so their part of the sum within 2^-17 max|v|; scores of d products in fp32, each within
+    # 2^-24 sum|q k| (1 + d), under 2^-24 * 129 * 3 * d^0.5 here after scaling (|q k| averages 2 / pi, its scaled sum
+    # stays below 3 d^0.5), 2^-12.4 at worst and a sixteenth of it, 2^-16, for sums that are rounded to nearest at
+    # random: 2^-13 max|v| holds all of it.
     cfg = config(2, N, 1, d, BF16, [D], [0], [0])
     parent = np.full((2, N), -1, np.int32) if D == 1 else np.array([[i - 5 if i >= 5 else -1 for i in range(N)]] * 2, np.int32)
     p = Problem(cfg, cap, [6, 17] if D == 1 else [43, 120 if cap > 200 else 52], parent, std=1.0)
-    if D > 1:
-        p.q[..., 0], p.k[..., 0] = 8.0, -100.0
     p.to_gpu()
     o, _ = p.step()
     ro, _ = p.reference()

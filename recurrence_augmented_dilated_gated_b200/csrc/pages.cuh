@@ -5,7 +5,8 @@
 
 namespace rat {
 
-// Quotients of a fixed divisor d >= 1 without a division: for n < 2^31,
+// Quotients of a fixed divisor d >= 1 without a division (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994): for n < 2^31,
 // n / d = hi32(n * m) >> s with m = ceil(2^(32 + s) / d), 2^s >= d (m < 2^33 has
 // its top bit implied: q = (hi32(n * (m - 2^32)) + n) >> s, and n + hi < 2^32).
 struct Divisor {

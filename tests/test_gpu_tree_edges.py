@@ -261,3 +261,15 @@ def test_fewer_pieces_than_the_capacity_has_runs(dtype):
     pos[5] = 7100
     p = Problem(cfg, cap, pos, random_parents(rng, B, N, 3)).to_gpu()
     p.check(*p.step())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_all_keys_of_a_head_in_one_item_where_pairs_are_many(dtype):
+    # 15104 pairs: no head is cut, however many rows it has; the item of a dense head writes the result itself
+    rng = np.random.default_rng(14)
+    B, H, N, cap = 59, 256, 2, 300
+    cfg = config(B, N, H, 64, dtype, [1, 1, 2, 1] * 64, [0, 200, 150, 3] * 64, [0, 1, 1, 1] * 64)
+    pos = [int(x) for x in rng.integers(0, 12, B)]
+    pos[7], pos[40] = 290, 131
+    p = Problem(cfg, cap, pos, random_parents(rng, B, N, 2)).to_gpu()
+    p.check(*p.step())
